@@ -17,6 +17,13 @@
  *   sparsesam_rcmlp  S4  fc1-GELU-fc2 on the kept tokens, added to the residual in place
  *   sparsesam_random_perm     S2 over random scores (the random-permutation ablation)
  *   sparsesam_keep_by_update  the keep-set by update magnitude (another keep criterion)
+ *   sparsesam_norm_residual   a block's post norm, gate, residual scale and residual add with the
+ *                             next block's pre norm; sparsesam_norm_residual_backward
+ *   sparsesam_expert_route    a token's top-k experts and weights; sparsesam_expert_route_backward
+ *   sparsesam_expert_sort     the assignments' stable order by expert
+ *   sparsesam_expert_gather, sparsesam_expert_combine  rows to that order and back with weights;
+ *                             sparsesam_expert_combine_backward
+ *   sparsesam_expert_mlp      the routed-expert MLP: sort, gather, both products, combine
  *
  * Conventions shared by every call
  *   - Pointers marked (device) are device memory owned by the caller; nothing is allocated or
@@ -62,8 +69,9 @@ extern "C" {
 #define SS_EWORKSPACE   (-3)  /* workspace pointer null/misaligned or smaller than required     */
 #define SS_ECUDA        (-4)  /* a CUDA runtime/driver call failed (launch, tensor-map encode)   */
 #define SS_ETIMEOUT     (-5)  /* a device-side wait gave up (read via sparsesam_device_status)   */
-#define SS_EINDEX       (-6)  /* a perm or keep index outside its unit or image reached a kernel;
-                                 the access was skipped (read via sparsesam_device_status)       */
+#define SS_EINDEX       (-6)  /* a perm or keep index outside its unit or image, or an expert id or
+                                 slot out of range, reached a kernel; the access was skipped
+                                 (read via sparsesam_device_status)                              */
 
 #define SS_GLOBAL 0
 #define SS_WINDOW 1
@@ -345,6 +353,151 @@ int sparsesam_encoder_stack(const ss_cfg* cfg, const float* lum, uint16_t* x, in
 int sparsesam_rcmlp_noalloc(const ss_cfg* cfg, uint16_t* x, int32_t C, int32_t hidden,
                             const uint16_t* w1, const uint16_t* b1, const uint16_t* w2,
                             const uint16_t* b2, const int32_t* keep, int32_t K, void* stream);
+
+/* ---- the norms around a block ---------------------------------------------------------------- */
+
+/* Element types of the norm and expert row calls. */
+#define SS_BF16 0
+#define SS_F16  1
+#define SS_F32  2
+
+#define SS_LAYERNORM 0   /* (v - mean) / sqrt(var + eps), biased variance */
+#define SS_RMSNORM   1   /* v / sqrt(mean(v^2) + eps)                     */
+
+typedef struct {
+  int64_t rows;           /* tokens, 0 <= rows < 2^31                                            */
+  int32_t C;              /* channels, a multiple of 8, at most 4096                             */
+  int32_t dtype;          /* SS_BF16, SS_F16 or SS_F32: the rows and the parameters              */
+  int32_t norm;           /* SS_LAYERNORM or SS_RMSNORM, of both norms                           */
+  float   eps;            /* > 0                                                                 */
+  int64_t rows_per_gate;  /* consecutive rows that share a gate row (an image's tokens); 0: no gate */
+  int64_t ld_y, ld_x, ld_n;  /* row strides in elements of y and dy; of x, x_out, dx_out and dx; of
+                                n and dn. 0: C. Otherwise at least C and a multiple of 8         */
+} ss_norm_cfg;
+
+/* What lies between two blocks of a residual stream, in one pass over the rows:
+ *   p     = post norm of y (post_w NULL: p = y)
+ *   x_out = x + gate[t / rows_per_gate] * scale * p      (gate, scale NULL: 1)
+ *   n     = pre norm of x_out (pre_w NULL: none; then n is NULL too)
+ * y: the block's output; x: the residual stream before it; n: what the next block reads. gate (device)
+ * [ceil(rows / rows_per_gate), C], scale, post_w, post_b, pre_w, pre_b (device) [C], the biases NULL for
+ * zero; rows (device) as cfg says, all of cfg's dtype and 16-byte aligned. Norms and sums in fp32; x_out
+ * is rounded once, n is the norm of x_out as stored (so it equals that of a separate call) and is
+ * rounded once. stats (device) fp32 [rows, 4] or NULL: the post norm's mean and 1/sqrt, then the pre
+ * norm's (0 for what is not there), which the backward reads. x_out may be x, and n may be y or x
+ * (not x_out), with the same stride; nothing else may overlap. Errors: SS_EINVAL (a NULL, misaligned
+ * or contradictory argument), SS_EUNSUPPORTED (C, rows). */
+int sparsesam_norm_residual(const ss_norm_cfg* cfg, const void* y, const void* x, const void* gate,
+                            const void* scale, const void* post_w, const void* post_b,
+                            const void* pre_w, const void* pre_b, void* x_out, void* n,
+                            float* stats, void* stream);
+
+/* Bytes of device workspace sparsesam_norm_residual_backward needs (0 on an invalid cfg, or for no
+ * rows). */
+size_t sparsesam_norm_residual_backward_workspace(const ss_norm_cfg* cfg);
+
+/* Gradients of sparsesam_norm_residual. y, x_out, gate, scale, post_w, post_b, pre_w: the forward's
+ * (x_out its result; it may be NULL without a pre norm), stats: what it wrote. dx_out: the gradient of
+ * x_out from what else reads it; dn: that of n (NULL without a pre norm). dx, dy (device): the
+ * gradients of x and y. dgate (device) fp32 [groups, C], dscale, dpost_w, dpost_b, dpre_w, dpre_b
+ * (device) fp32 [C]: the parameters' gradients, summed in fp32 over the rows in a fixed order (the
+ * same inputs give the same bits); each may be NULL if it is not wanted, and is NULL where its
+ * parameter is (dpost_b and dpre_b need post_w and pre_w only). They are written, not added to; with
+ * no rows they are zero. dx may be dx_out, and dy may be y, else no output may overlap anything. ws
+ * (device, 256-byte aligned) >= sparsesam_norm_residual_backward_workspace(cfg) bytes. */
+int sparsesam_norm_residual_backward(const ss_norm_cfg* cfg, const void* y, const void* x_out,
+                                     const void* gate, const void* scale, const void* post_w,
+                                     const void* post_b, const void* pre_w, const float* stats,
+                                     const void* dx_out, const void* dn, void* dx, void* dy,
+                                     float* dgate, float* dscale, float* dpost_w, float* dpost_b,
+                                     float* dpre_w, float* dpre_b, void* ws, size_t ws_bytes,
+                                     void* stream);
+
+/* ---- routed experts --------------------------------------------------------------------------- */
+
+/* Where the RC-MLP sends the kept tokens through one MLP, a routed-expert MLP sends each token through
+ * topk of `experts` MLPs. Assignment a = t * topk + j is token t's j-th expert; n = tokens * topk. */
+typedef struct {
+  int32_t tokens;    /* rows, >= 0; tokens * topk < 2^30                                        */
+  int32_t experts;   /* 1 .. 512                                                                */
+  int32_t topk;      /* experts of a token, 1 .. min(experts, 16)                               */
+  int32_t C;         /* channels, a multiple of 8 (calls that move rows)                        */
+  int32_t hidden;    /* the experts' hidden width, a multiple of 8 (sparsesam_expert_mlp)       */
+  int32_t dtype;     /* SS_BF16, SS_F16 or SS_F32 rows; sparsesam_expert_mlp: SS_BF16           */
+  int64_t ld;        /* row stride in elements of the token-order rows (x, residual, out, dout);
+                        0: C. Otherwise at least C and a multiple of 8. Sorted rows are C apart */
+} ss_expert_cfg;
+
+/* The router. logits (device) fp32 [tokens, experts] -> ids (device) int32 [tokens, topk]: the
+ * token's topk largest logits in descending order, equal ones lower expert first; weight (device) fp32
+ * [tokens, topk]: softmax over all of the token's logits at ids (renorm == 0), or over the chosen ones
+ * only (renorm != 0). A logit of -inf, or NaN, closes its expert to the token; where fewer than topk are
+ * open, the rest of the row has id -1 and weight 0. (+inf gives NaN weights, as softmax does.) */
+int sparsesam_expert_route(const ss_expert_cfg* cfg, const float* logits, int32_t renorm,
+                           int32_t* ids, float* weight, void* stream);
+
+/* Gradient of weight for the logits: dweight (device) fp32 [tokens, topk] -> dlogits (device) fp32
+ * [tokens, experts], every entry written. logits, ids, weight as the forward had and wrote them (logits
+ * may be NULL with renorm). dweight at an id of -1 is not read; an id outside [-1, experts) records
+ * SS_EINDEX and counts as -1. */
+int sparsesam_expert_route_backward(const ss_expert_cfg* cfg, const float* logits, int32_t renorm,
+                                    const int32_t* ids, const float* weight, const float* dweight,
+                                    float* dlogits, void* stream);
+
+/* Bytes of device workspace sparsesam_expert_sort needs (0: none, or an invalid cfg). */
+size_t sparsesam_expert_sort_workspace(const ss_expert_cfg* cfg);
+
+/* The assignments in a stable order by expert. ids (device) int32 [tokens, topk], -1: routed nowhere (an
+ * id outside [-1, experts) records SS_EINDEX and counts as -1). offsets (device) int32 [experts + 1]:
+ * expert e has the places offsets[e] .. offsets[e+1] - 1, offsets[experts] = the assignments routed.
+ * order (device) int32 [n]: the assignment at each place, ascending within an expert; -1 at the places
+ * past the last. slot (device) int32 [tokens, topk]: the inverse, each assignment's place or -1. Any of
+ * the three outputs may be NULL (not all). ws (device, 256-byte aligned) >=
+ * sparsesam_expert_sort_workspace(cfg) bytes. */
+int sparsesam_expert_sort(const ss_expert_cfg* cfg, const int32_t* ids, int32_t* order,
+                          int32_t* slot, int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows to the sorted order: xs[slot[t, j]] = x[t]. x (device) [tokens, C], xs (device) [n, C], 16-byte
+ * aligned; slot (device) from sparsesam_expert_sort, its places distinct: one outside [-1, n) records
+ * SS_EINDEX and is skipped. Rows of xs at no slot are left as they were. The gradient of x is
+ * sparsesam_expert_combine of the gradient of xs without weights or residual. */
+int sparsesam_expert_gather(const ss_expert_cfg* cfg, const void* x, const int32_t* slot, void* xs,
+                            void* stream);
+
+/* And back: out[t] = residual[t] + sum_j weight[t, j] * ys[slot[t, j]]. The sum in fp32 in the order of
+ * j, then the residual, rounded once; slots of -1 are left out, whatever their weight. ys (device)
+ * [n, C]; weight (device) fp32 [tokens, topk] or NULL (1); residual (device) [tokens, C] or NULL (0);
+ * out (device) [tokens, C], may be residual. slot as in sparsesam_expert_gather. */
+int sparsesam_expert_combine(const ss_expert_cfg* cfg, const void* ys, const int32_t* slot,
+                             const float* weight, const void* residual, void* out, void* stream);
+
+/* Gradients of sparsesam_expert_combine (the residual's is dout itself): dys[slot[t, j]] = weight[t, j] *
+ * dout[t], rounded once, and dweight[t, j] = dout[t] . ys[slot[t, j]] in fp32 (0 at a slot of -1). dout
+ * (device) [tokens, C]; ys, dys (device) [n, C], dys may be ys; rows of dys at no slot are left as they
+ * were. */
+int sparsesam_expert_combine_backward(const ss_expert_cfg* cfg, const void* dout, const void* ys,
+                                      const int32_t* slot, const float* weight, void* dys,
+                                      float* dweight, void* stream);
+
+/* Bytes of device workspace sparsesam_expert_mlp needs (0 on an invalid cfg, or for no tokens). */
+size_t sparsesam_expert_mlp_workspace(const ss_expert_cfg* cfg);
+
+/* The routed-expert MLP, forward:
+ *   out[t] = residual[t] + sum_j weight[t, j] * (w2_e . GELU(w1_e . x[t] + b1_e) + b2_e), e = ids[t, j]
+ * with the GELU of sparsesam_rcmlp. x, residual (NULL: 0), out (device) bf16 [tokens, C], row stride
+ * cfg->ld; ids (device) int32 [tokens, topk], weight (device) fp32 [tokens, topk] (NULL: 1) from
+ * sparsesam_expert_route; w1 (device) bf16 [experts, hidden, C], b1 [experts, hidden], w2 [experts, C,
+ * hidden], b2 [experts, C], the biases NULL for zero; x, residual, out, w1, w2 16-byte aligned. An id of -1
+ * routes nowhere (one outside [-1, experts) too, and records SS_EINDEX): a token without any gets
+ * its residual. Any number of tokens, one included, spread over the experts in any way. bf16 operands, fp32
+ * accumulation; the hidden rows are rounded to bf16 between the products, and so is each expert's
+ * output row before it is weighted unless the second product was split along its K (a few rows). out
+ * may be x or residual. ws (device, 256-byte aligned) >= sparsesam_expert_mlp_workspace(cfg) bytes, its
+ * contents on entry do not matter; calls that may run at once need one each. */
+int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int32_t* ids,
+                         const float* weight, const uint16_t* residual, const uint16_t* w1,
+                         const uint16_t* b1, const uint16_t* w2, const uint16_t* b2,
+                         uint16_t* out, void* ws, size_t ws_bytes, void* stream);
 
 /* Reads (and clears) the device status word that bounded device waits and index checks write.
  * Synchronises the given stream. *status receives SS_OK, SS_ETIMEOUT or SS_EINDEX. Returns SS_OK or

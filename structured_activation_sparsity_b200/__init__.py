@@ -24,12 +24,20 @@ _LIB_NAMES = {
     "sparsesam_encoder_stack_workspace", "sparsesam_attn_partial",
     "sparsesam_attn_partial_workspace", "sparsesam_attn_relpos", "sparsesam_attn_relpos_workspace",
     "sparsesam_trace_start", "sparsesam_trace_stop", "strerror",
+    "SS_BF16", "SS_F16", "SS_F32", "SS_LAYERNORM", "SS_RMSNORM", "SsNormCfg", "SsExpertCfg",
+    "make_norm_cfg", "make_expert_cfg", "sparsesam_norm_residual",
+    "sparsesam_norm_residual_backward", "sparsesam_norm_residual_backward_workspace",
+    "sparsesam_expert_route", "sparsesam_expert_route_backward", "sparsesam_expert_sort",
+    "sparsesam_expert_sort_workspace", "sparsesam_expert_gather", "sparsesam_expert_combine",
+    "sparsesam_expert_combine_backward", "sparsesam_expert_mlp", "sparsesam_expert_mlp_workspace",
 }
 
 
 def __getattr__(name):
     if name in _LIB_NAMES:
-        return getattr(importlib.import_module("._lib", __name__), name)
+        # kept, so that later uses are plain attribute look-ups
+        value = globals()[name] = getattr(importlib.import_module("._lib", __name__), name)
+        return value
     if name == "HotPath":
         return importlib.import_module(".hotpath", __name__).HotPath
     raise AttributeError(name)

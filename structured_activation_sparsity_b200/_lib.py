@@ -21,6 +21,8 @@ SS_ETIMEOUT = -5
 SS_EINDEX = -6
 SS_GLOBAL = 0
 SS_WINDOW = 1
+SS_BF16, SS_F16, SS_F32 = 0, 1, 2
+SS_LAYERNORM, SS_RMSNORM = 0, 1
 
 
 class SsCfg(ctypes.Structure):
@@ -44,6 +46,19 @@ class SsBlockWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in BLOCK_WEIGHT_FIELDS]
 
 
+class SsNormCfg(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("norm", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("rows_per_gate", ctypes.c_int64), ("ld_y", ctypes.c_int64),
+                ("ld_x", ctypes.c_int64), ("ld_n", ctypes.c_int64)]
+
+
+class SsExpertCfg(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("C", ctypes.c_int32), ("hidden", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("ld", ctypes.c_int64)]
+
+
 class SparseSAMError(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -57,6 +72,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, VP = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
     cfgp = ctypes.POINTER(SsCfg)
+    xcfgp = ctypes.POINTER(SsExpertCfg)
     sig = {
         "sparsesam_pattern": (ctypes.c_int, [cfgp, ctypes.POINTER(SsPattern)]),
         "sparsesam_blocklist": (ctypes.c_int, [cfgp, P, P, I32]),
@@ -85,6 +101,19 @@ def _load():
         "sparsesam_encoder_stack_workspace": (SZ, [cfgp, I32, I32]),
         "sparsesam_encoder_stack": (ctypes.c_int, [cfgp, P, P, I32, I32, I32,
                                                    ctypes.POINTER(SsBlockWeights), P, P, SZ, VP]),
+        "sparsesam_norm_residual": (ctypes.c_int, [ctypes.POINTER(SsNormCfg)] + [P] * 11 + [VP]),
+        "sparsesam_norm_residual_backward_workspace": (SZ, [ctypes.POINTER(SsNormCfg)]),
+        "sparsesam_norm_residual_backward": (ctypes.c_int, [ctypes.POINTER(SsNormCfg)] + [P] * 19 +
+                                             [SZ, VP]),
+        "sparsesam_expert_route": (ctypes.c_int, [xcfgp, P, I32, P, P, VP]),
+        "sparsesam_expert_route_backward": (ctypes.c_int, [xcfgp, P, I32, P, P, P, P, VP]),
+        "sparsesam_expert_sort_workspace": (SZ, [xcfgp]),
+        "sparsesam_expert_sort": (ctypes.c_int, [xcfgp, P, P, P, P, P, SZ, VP]),
+        "sparsesam_expert_gather": (ctypes.c_int, [xcfgp, P, P, P, VP]),
+        "sparsesam_expert_combine": (ctypes.c_int, [xcfgp, P, P, P, P, P, VP]),
+        "sparsesam_expert_combine_backward": (ctypes.c_int, [xcfgp, P, P, P, P, P, P, VP]),
+        "sparsesam_expert_mlp_workspace": (SZ, [xcfgp]),
+        "sparsesam_expert_mlp": (ctypes.c_int, [xcfgp] + [P] * 10 + [SZ, VP]),
         "sparsesam_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
         "sparsesam_wait_selftest": (ctypes.c_int, [I32, VP]),
         "sparsesam_device_status": (ctypes.c_int, [ctypes.POINTER(I32), VP]),
@@ -303,6 +332,117 @@ def sparsesam_encoder_stack(cfg, lum, x, C, hidden, weights, is_global, ws, ws_b
                   lib.sparsesam_encoder_stack(ctypes.byref(cfg), _ptr(lum), _ptr(x), int(C),
                                               int(hidden), n, arr, ctypes.addressof(flags),
                                               _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def _dtype(dtype) -> int:
+    """The SS_* code of a dtype: the code itself, "bf16" / "f16" / "f32" or a torch dtype."""
+    if isinstance(dtype, int):
+        return dtype
+    name = str(dtype).replace("torch.", "")
+    codes = {"bf16": SS_BF16, "bfloat16": SS_BF16, "f16": SS_F16, "float16": SS_F16,
+             "f32": SS_F32, "float32": SS_F32}
+    if name not in codes:
+        raise ValueError(f"unsupported dtype {dtype!r}")
+    return codes[name]
+
+
+def make_norm_cfg(rows, C, dtype="bf16", norm="layer", eps=1e-6, rows_per_gate=0, ld_y=0, ld_x=0,
+                  ld_n=0) -> SsNormCfg:
+    """norm: "layer" or "rms" (or the SS_* code); strides in elements, 0 for dense rows."""
+    kind = norm if isinstance(norm, int) else {"layer": SS_LAYERNORM, "rms": SS_RMSNORM}[norm]
+    return SsNormCfg(rows, C, _dtype(dtype), kind, eps, rows_per_gate, ld_y, ld_x, ld_n)
+
+
+def make_expert_cfg(tokens, experts, topk, C=0, hidden=0, dtype="bf16", ld=0) -> SsExpertCfg:
+    return SsExpertCfg(tokens, experts, topk, C, hidden, _dtype(dtype), ld)
+
+
+def sparsesam_norm_residual(cfg, y, x, gate, scale, post_w, post_b, pre_w, pre_b, x_out, n, stats,
+                            stream=None):
+    """x_out = x + gate * scale * post norm(y), n = pre norm(x_out); absent parameters are None."""
+    return _check("sparsesam_norm_residual",
+                  lib.sparsesam_norm_residual(ctypes.byref(cfg), _ptr(y), _ptr(x), _ptr(gate),
+                                              _ptr(scale), _ptr(post_w), _ptr(post_b),
+                                              _ptr(pre_w), _ptr(pre_b), _ptr(x_out), _ptr(n),
+                                              _ptr(stats), _stream(stream)))
+
+
+def sparsesam_norm_residual_backward_workspace(cfg) -> int:
+    return int(lib.sparsesam_norm_residual_backward_workspace(ctypes.byref(cfg)))
+
+
+def sparsesam_norm_residual_backward(cfg, y, x_out, gate, scale, post_w, post_b, pre_w, stats,
+                                     dx_out, dn, dx, dy, dgate, dscale, dpost_w, dpost_b, dpre_w,
+                                     dpre_b, ws, ws_bytes, stream=None):
+    """Row gradients dx, dy and the parameters' fp32 gradients (None: not wanted)."""
+    return _check("sparsesam_norm_residual_backward",
+                  lib.sparsesam_norm_residual_backward(
+                      ctypes.byref(cfg), _ptr(y), _ptr(x_out), _ptr(gate), _ptr(scale),
+                      _ptr(post_w), _ptr(post_b), _ptr(pre_w), _ptr(stats), _ptr(dx_out), _ptr(dn),
+                      _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dscale), _ptr(dpost_w), _ptr(dpost_b),
+                      _ptr(dpre_w), _ptr(dpre_b), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def sparsesam_expert_route(cfg, logits, renorm, ids, weight, stream=None):
+    """The topk experts of each token and their softmax weights (renorm: over the chosen only)."""
+    return _check("sparsesam_expert_route",
+                  lib.sparsesam_expert_route(ctypes.byref(cfg), _ptr(logits), int(renorm),
+                                             _ptr(ids), _ptr(weight), _stream(stream)))
+
+
+def sparsesam_expert_route_backward(cfg, logits, renorm, ids, weight, dweight, dlogits,
+                                    stream=None):
+    return _check("sparsesam_expert_route_backward",
+                  lib.sparsesam_expert_route_backward(ctypes.byref(cfg), _ptr(logits), int(renorm),
+                                                      _ptr(ids), _ptr(weight), _ptr(dweight),
+                                                      _ptr(dlogits), _stream(stream)))
+
+
+def sparsesam_expert_sort_workspace(cfg) -> int:
+    return int(lib.sparsesam_expert_sort_workspace(ctypes.byref(cfg)))
+
+
+def sparsesam_expert_sort(cfg, ids, order, slot, offsets, ws, ws_bytes, stream=None):
+    """The assignments in a stable order by expert (order, slot, offsets: None to skip one)."""
+    return _check("sparsesam_expert_sort",
+                  lib.sparsesam_expert_sort(ctypes.byref(cfg), _ptr(ids), _ptr(order), _ptr(slot),
+                                            _ptr(offsets), _ptr(ws), int(ws_bytes),
+                                            _stream(stream)))
+
+
+def sparsesam_expert_gather(cfg, x, slot, xs, stream=None):
+    """xs[slot[t, j]] = x[t]; its gradient is sparsesam_expert_combine without weights."""
+    return _check("sparsesam_expert_gather",
+                  lib.sparsesam_expert_gather(ctypes.byref(cfg), _ptr(x), _ptr(slot), _ptr(xs),
+                                              _stream(stream)))
+
+
+def sparsesam_expert_combine(cfg, ys, slot, weight, residual, out, stream=None):
+    """out[t] = residual[t] + sum_j weight[t, j] * ys[slot[t, j]] (None: weights 1, residual 0)."""
+    return _check("sparsesam_expert_combine",
+                  lib.sparsesam_expert_combine(ctypes.byref(cfg), _ptr(ys), _ptr(slot),
+                                               _ptr(weight), _ptr(residual), _ptr(out),
+                                               _stream(stream)))
+
+
+def sparsesam_expert_combine_backward(cfg, dout, ys, slot, weight, dys, dweight, stream=None):
+    return _check("sparsesam_expert_combine_backward",
+                  lib.sparsesam_expert_combine_backward(ctypes.byref(cfg), _ptr(dout), _ptr(ys),
+                                                        _ptr(slot), _ptr(weight), _ptr(dys),
+                                                        _ptr(dweight), _stream(stream)))
+
+
+def sparsesam_expert_mlp_workspace(cfg) -> int:
+    return int(lib.sparsesam_expert_mlp_workspace(ctypes.byref(cfg)))
+
+
+def sparsesam_expert_mlp(cfg, x, ids, weight, residual, w1, b1, w2, b2, out, ws, ws_bytes,
+                         stream=None):
+    """The routed-expert MLP over tokens x with the router's ids and weights."""
+    return _check("sparsesam_expert_mlp",
+                  lib.sparsesam_expert_mlp(ctypes.byref(cfg), _ptr(x), _ptr(ids), _ptr(weight),
+                                           _ptr(residual), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2),
+                                           _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
 def sparsesam_set_wait_limit_ns(ns: int):

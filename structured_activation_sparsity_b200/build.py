@@ -15,8 +15,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparsesam.so")
-SOURCES = ["score_perm.cu", "attn.cu", "mlp.cu", "block.cu", "partial.cu", "relpos.cu", "api.cu", "noalloc.cu"]
-HEADERS = ["common.cuh", "kernels.h", "pattern.h"]
+SOURCES = ["score_perm.cu", "attn.cu", "mlp.cu", "block.cu", "partial.cu", "relpos.cu", "api.cu", "noalloc.cu",
+           "norm.cu", "experts.cu", "expert_mlp.cu", "api_experts.cu"]
+HEADERS = ["common.cuh", "rows.cuh", "host.h", "kernels.h", "pattern.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

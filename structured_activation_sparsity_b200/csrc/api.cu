@@ -9,6 +9,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "host.h"
 #include "kernels.h"
 
 namespace ss {
@@ -49,6 +50,8 @@ namespace {
 std::mutex g_mu;
 std::atomic<uint64_t> g_launches{0};
 
+}  // namespace
+
 // ---- per-device address of the status word ----------------------------------------------------
 int* status_word() {
   static int* addr[128] = {};
@@ -64,6 +67,8 @@ int* status_word() {
 }
 
 // ---- launch tracing -----------------------------------------------------------------------------
+namespace {
+
 struct TraceRec {
   const char* name;
   cudaEvent_t e0, e1;
@@ -73,21 +78,21 @@ std::vector<TraceRec> g_trace;
 int g_trace_used = 0;
 bool g_tracing = false;
 
-template <class F>
-cudaError_t traced(const char* name, cudaStream_t st, F&& f) {
-  TraceRec* rec = nullptr;
-  if (g_tracing && g_trace_used < (int)g_trace.size()) {
-    rec = &g_trace[g_trace_used++];
-    rec->name = name;
-    cudaEventRecord(rec->e0, st);
-  }
-  cudaError_t e = f();
-  if (rec) cudaEventRecord(rec->e1, st);
-  g_launches.fetch_add(1, std::memory_order_relaxed);
-  return e;
+}  // namespace
+
+int trace_open(const char* name, cudaStream_t st) {
+  if (!g_tracing || g_trace_used >= (int)g_trace.size()) return -1;
+  const int rec = g_trace_used++;
+  g_trace[rec].name = name;
+  cudaEventRecord(g_trace[rec].e0, st);
+  return rec;
 }
+void trace_close(int rec, cudaStream_t st) { cudaEventRecord(g_trace[rec].e1, st); }
+void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 // ---- tensor maps --------------------------------------------------------------------------------
+namespace {
+
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -107,8 +112,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// bf16 tensor of `mats` matrices [rows, inner] with rows `row_bytes` apart; box [box_rows, box_inner].
-// `rank` must match the dimensionality of the kernel's TMA instruction (2: one matrix, 3: a stack).
+}  // namespace
+
 bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* base, uint64_t inner, uint64_t rows,
                  uint64_t mats, uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows,
                  CUtensorMapSwizzle sw) {
@@ -126,6 +131,8 @@ bool encode_bf16(CUtensorMap* m, cuuint32_t rank, const void* base, uint64_t inn
 }
 
 // ---- geometry -----------------------------------------------------------------------------------
+namespace {
+
 struct Geo {
   int B, Hg, Wg, T;      // images, grid, tokens per image
   int window_mode, ws, wpr, windows;
@@ -180,15 +187,6 @@ int pattern_of(const ss_cfg* c, const Geo& g, ss_pattern* p) {
   p->rho = (double)p->nnz / (double)(nb * nb);
   return SS_OK;
 }
-
-inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-int cuda_err(cudaError_t e) { return e == cudaSuccess ? SS_OK : SS_ECUDA; }
-
-// The GEMM and attention work splits are planned for the B200's 148 SMs, so workspace sizes do
-// not depend on the device a call runs on; launches use min(units, the device's SMs) CTAs.
-constexpr int kPlanSMs = 148;
 
 // The attention workspace: the gathered Q, K and V ([U*heads, N, dh] bf16 each); for the pair
 // kernel its permuted output Op (the same layout), and, when it splits pairs into pieces, its
@@ -256,6 +254,8 @@ size_t rcmlp_ws_bytes(const Geo& g, int K, int C, int hidden) {
   return mlp_plan(g, K, C, hidden).total;
 }
 
+}  // namespace
+
 int sm_count() {
   static int cached[128] = {};
   int dev = 0;
@@ -269,7 +269,6 @@ int sm_count() {
   return cached[dev];
 }
 
-}  // namespace
 }  // namespace ss
 
 using namespace ss;
@@ -1127,7 +1126,8 @@ uint64_t sparsesam_launch_count(void) { return g_launches.load(); }
 int sparsesam_set_wait_limit_ns(uint64_t ns) {
   const uint64_t v = ns ? ns : kWaitLimitNs;
   if (set_wait_limit_here(v) != cudaSuccess || set_wait_limit_attn(v) != cudaSuccess ||
-      set_wait_limit_mlp(v) != cudaSuccess)
+      set_wait_limit_mlp(v) != cudaSuccess || set_wait_limit_norm(v) != cudaSuccess ||
+      set_wait_limit_expert_mlp(v) != cudaSuccess)
     return SS_ECUDA;
   return SS_OK;
 }
@@ -1189,7 +1189,7 @@ const char* sparsesam_strerror(int code) {
     case SS_EWORKSPACE: return "workspace missing, misaligned or too small";
     case SS_ECUDA: return "CUDA call failed";
     case SS_ETIMEOUT: return "device wait timed out";
-    case SS_EINDEX: return "perm or keep index outside its unit or image (access skipped)";
+    case SS_EINDEX: return "perm, keep or expert index out of range (access skipped)";
   }
   return "unknown error";
 }

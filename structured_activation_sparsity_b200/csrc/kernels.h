@@ -10,11 +10,14 @@
 
 namespace ss {
 
+constexpr int kRowCtas = 148;           // CTAs the persistent row kernels are planned for (B200's SMs)
 constexpr int kMaxRankTokens = 16384;   // tokens per unit the rank kernel holds in shared memory
 
 // The bounded-wait limit of each source file's kernels (see c_wait_limit_ns), current device.
 cudaError_t set_wait_limit_attn(uint64_t ns);
 cudaError_t set_wait_limit_mlp(uint64_t ns);
+cudaError_t set_wait_limit_norm(uint64_t ns);
+cudaError_t set_wait_limit_expert_mlp(uint64_t ns);
 
 // sparsesam_rcmlp's argument checks (same codes, same order) and its workspace bytes in *need.
 int rcmlp_validate(const ss_cfg* cfg, const uint16_t* x, int32_t C, int32_t hidden,
@@ -194,5 +197,95 @@ size_t gemm_partial_bytes(const GemmPlan& p);
 cudaError_t launch_gemm(const CUtensorMap* ta, const CUtensorMap* tb, const GemmPlan& p, int M,
                         int N, int Kd, const GemmEpilogue& ep, float* partial, int* counters,
                         int sms, int* status, cudaStream_t st);
+
+// ---- the norms around a block, with its gate, residual scale and residual add ---------------------
+
+constexpr int kMaxNormC = 4096;       // channels of a row: 512 threads of eight hold it
+constexpr int kNormMaxCtas = kRowCtas;
+
+struct NormParams {
+  const void *y, *x, *gate, *scale, *post_w, *post_b, *pre_w, *pre_b;
+  void *x_out, *n;
+  float* stats;                        // [rows, 4] or null
+  long long rows, rows_per_gate, ld_y, ld_x, ld_n;
+  int C, center;                       // center: LayerNorm (else RMS norm)
+  float eps;
+};
+cudaError_t launch_norm_residual(const NormParams& p, int dtype, cudaStream_t st);
+
+struct NormBwdParams {
+  const void *y, *x, *gate, *scale, *post_w, *post_b, *pre_w;   // x: the forward's x_out
+  const float* stats;
+  const void *dx_out, *dn;
+  void *dx, *dy;
+  float *dgate, *dscale, *dpost_w, *dpost_b, *dpre_w, *dpre_b;  // each may be null
+  float* partial;                      // [CTAs][4][C]
+  float* gate_partial;                 // [workers][2][C] (with a gate)
+  long long rows, rows_per_gate, ld_y, ld_x, ld_n;
+  int C, center;
+};
+// Bytes of the two partials; *gate_offset: where the second begins.
+size_t norm_backward_partial(long long rows, int C, int es, bool pre, bool gate,
+                             size_t* gate_offset);
+// Row gradients and the partial column sums (nothing at rows == 0).
+cudaError_t launch_norm_backward(const NormBwdParams& p, int dtype, int* status, cudaStream_t st);
+// The parameters' gradients from the partials.
+cudaError_t launch_norm_reduce(const NormBwdParams& p, int dtype, cudaStream_t st);
+
+// ---- routed experts --------------------------------------------------------------------------------
+
+constexpr int kMaxExperts = 512;
+constexpr int kMaxTopk = 16;
+constexpr int kSortOne = 4096;         // assignments one CTA sorts by itself
+constexpr int kSortMaxCtas = kRowCtas;
+
+cudaError_t launch_expert_route(const float* logits, int32_t* ids, float* weight, int T, int E,
+                                int topk, bool renorm, cudaStream_t st);
+cudaError_t launch_expert_route_backward(const float* logits, const int32_t* ids,
+                                         const float* weight, const float* dweight, float* dlogits,
+                                         int T, int E, int topk, bool renorm, int* status,
+                                         cudaStream_t st);
+// The sort of n assignments: launch_expert_count (into hist [sort_ctas(n)][E]) when it takes more than one CTA,
+// then launch_expert_place.
+int sort_ctas(long long n);
+cudaError_t launch_expert_count(const int32_t* ids, int32_t* hist, int n, int E, int* status,
+                                cudaStream_t st);
+cudaError_t launch_expert_place(const int32_t* ids, const int32_t* hist, int32_t* order,
+                                int32_t* slot, int32_t* offsets, int n, int E, int* status,
+                                cudaStream_t st);
+// Rows x, residual, out and dout are ld elements apart; the sorted rows are C apart.
+cudaError_t launch_expert_gather(const void* x, const int32_t* slot, void* xs, int tokens,
+                                 int topk, int C, long long ld, int dtype, int* status,
+                                 cudaStream_t st);
+// splits > 0: ys holds that many fp32 partials [tokens * topk, C].
+cudaError_t launch_expert_combine(const void* ys, const int32_t* slot, const float* weight,
+                                  const void* residual, void* out, int tokens, int topk, int C,
+                                  long long ld, int dtype, int splits, int* status,
+                                  cudaStream_t st);
+cudaError_t launch_expert_combine_backward(const void* dout, const void* ys, const int32_t* slot,
+                                           const float* weight, void* dys, float* dweight,
+                                           int tokens, int topk, int C, long long ld, int dtype,
+                                           int* status, cudaStream_t st);
+
+// One product of all experts: rows [n, Kd] sorted by expert (offsets [E + 1], on the device) times
+// W_e [features, Kd]^T. out: bf16 [n, features], with the bias and, if set, the GELU; or partial: fp32
+// [splits][n, features], the bias in the first.
+struct ExpertGemm {
+  const int32_t* offsets;
+  const uint16_t* bias;    // [E, features] or null
+  uint16_t* out;
+  float* partial;
+  long long n;
+  int E, features, m_tiles, splits, kb_total, gelu;
+};
+struct ExpertGemmPlan {
+  int tn, m_tiles, splits;   // token tile, feature tiles, k-splits
+  long long max_units;       // at most
+};
+ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms);
+// ta: weights [E * features, Kd], box 128 rows; tb: rows [n, Kd], box p.tn rows; both 64 columns.
+cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
+                               const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
+                               cudaStream_t st);
 
 }  // namespace ss
