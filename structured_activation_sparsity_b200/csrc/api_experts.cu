@@ -130,9 +130,11 @@ int sparsesam_norm_residual(const ss_norm_cfg* cfg, const void* y, const void* x
   p.C = cfg->C;
   p.center = cfg->norm == SS_LAYERNORM;
   p.eps = cfg->eps;
+  int* status = status_word();
+  if (!status) return SS_ECUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_err(traced("norm_residual", st, [&] {
-    return launch_norm_residual(p, cfg->dtype, st);
+    return launch_norm_residual(p, cfg->dtype, status, st);
   }));
 }
 

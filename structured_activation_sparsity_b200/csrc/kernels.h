@@ -211,7 +211,8 @@ struct NormParams {
   int C, center;                       // center: LayerNorm (else RMS norm)
   float eps;
 };
-cudaError_t launch_norm_residual(const NormParams& p, int dtype, cudaStream_t st);
+constexpr int kNormDirectRows = 1024;  // up to this many rows, the forward takes the direct kernel
+cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cudaStream_t st);
 
 struct NormBwdParams {
   const void *y, *x, *gate, *scale, *post_w, *post_b, *pre_w;   // x: the forward's x_out

@@ -6,181 +6,435 @@
 //   n     = pre norm of x_out as stored         (what the next block reads)
 //
 // Both directions are bound by HBM: every row is read and written once, all sums stay in fp32.
+#include <type_traits>
+
 #include "kernels.h"
 #include "rows.cuh"
 
 namespace ss {
 
+// ---- pairs ------------------------------------------------------------------------------------
+// Eight fp32 channels as four packed pairs: the arithmetic below runs two channels an instruction.
+struct F8 {
+  uint64_t p[4];
+};
+__device__ __forceinline__ uint64_t f2_same(float a) { return f2_pack(a, a); }
+__device__ __forceinline__ void f8_fill(F8& f, float a) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_same(a);
+}
+template <class T>
+__device__ __forceinline__ void f8_unpack(const Chunk<T>& c, F8& f) {
+  float v[8];
+  chunk_floats(c, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.p[i] = f2_pack(v[2 * i], v[2 * i + 1]);
+}
+template <class T>
+__device__ __forceinline__ void f8_store(typename T::Store* ptr, const F8& f) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f.p[i], v[2 * i], v[2 * i + 1]);
+  Chunk<T> c;
+  chunk_round(c, v);
+  chunk_store(ptr, c);
+}
+// Rounds f to the element type, stores it and keeps the stored values.
+template <class T>
+__device__ __forceinline__ void f8_round(F8& f, typename T::Store* ptr) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(f.p[i], v[2 * i], v[2 * i + 1]);
+  Chunk<T> c;
+  chunk_round(c, v);
+  chunk_store(ptr, c);
+  f8_unpack(c, f);
+}
+// To and from a vector of C fp32 in shared memory, channels c .. c + 7: the chunks' first halves lie side
+// by side, then their second halves, so that the lanes of a warp read 16 bytes next to each other
+// (eight consecutive floats a lane would meet in the banks: 46 instead of 35 us for the ViT-H batch).
+__device__ __forceinline__ void f8_put(float* to, int C, int c, const F8& f) {
+  *reinterpret_cast<ulonglong2*>(to + c / 2) = make_ulonglong2(f.p[0], f.p[1]);
+  *reinterpret_cast<ulonglong2*>(to + C / 2 + c / 2) = make_ulonglong2(f.p[2], f.p[3]);
+}
+__device__ __forceinline__ void f8_get(F8& f, const float* from, int C, int c) {
+  const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(from + c / 2);
+  const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(from + C / 2 + c / 2);
+  f.p[0] = a.x;
+  f.p[1] = a.y;
+  f.p[2] = b.x;
+  f.p[3] = b.y;
+}
+// The four pairs' sum.
+__device__ __forceinline__ float f8_sum(const F8& f) {
+  float a, b;
+  f2_unpack(f2_add(f2_add(f.p[0], f.p[1]), f2_add(f.p[2], f.p[3])), a, b);
+  return a + b;
+}
+
 // ---- forward --------------------------------------------------------------------------------
-// `wpr` warps hold a row, V chunks of eight channels a lane (chunk (e * wpr + warp) * 32 + lane), so
-// the row stays in registers from its load to the second norm. Mean, then the sum of squared
-// deviations from it (two passes over registers): no cancellation at a large mean.
-template <class T, int V>
-__global__ void __launch_bounds__(256) k_norm_residual(const NormParams p, int wpr) {
-  __shared__ float red[2][8];
-  griddep_wait();
-  griddep_launch();
-  using S = typename T::Store;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rpb = 8 / wpr, wr = warp % wpr;
-  const long long row = (long long)blockIdx.x * rpb + warp / wpr;
-  const bool live = row < p.rows;
-  const int chunks = p.C / 8;
-  int buf = 0;
-  // Sum over the row's lanes (wpr > 1: through shared memory, two buffers in turn).
-  auto row_sum = [&](float s) {
-    s = warp_sum(s);
-    if (wpr > 1) {
-      if (lane == 0) red[buf][warp] = s;
-      __syncthreads();
-      s = 0.f;
-      for (int i = 0; i < wpr; ++i) s += red[buf][warp - wr + i];
-      buf ^= 1;
-    }
-    return s;
+// A norm's mean and 1/sqrt over a row that `wpr` warps hold, V chunks a lane, n_w channels in warp w.
+// Each warp takes its sum and its sum of squared deviations from its own mean; those are joined by
+//   M2 = sum_w M2_w + n_w (mean_w - mean)^2
+// (Chan, Golub and LeVeque's update), so no large mean cancels and one meeting of the warps is enough.
+// LPR lanes share a row (fewer than 32: several rows a warp). chunk(e): whether chunk e is in the row (the
+// others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another.
+template <int V, int LPR, class Live, class Meet>
+__device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int C, int wpr, int wr,
+                                            bool center, float eps, float2* red, Meet&& meet,
+                                            float& mean, float& rstd) {
+  const float inv_c = 1.0f / (float)C;
+  // Channels of warp w of the row: its span of V * 256.
+  auto held = [&](int w) {
+    const int left = C - w * V * 256;
+    return (float)(left > V * 256 ? V * 256 : left > 0 ? left : 0);
   };
-  float v[V][8];
-  Chunk<T> xr[V];
-  const S* yrow = static_cast<const S*>(p.y) + row * p.ld_y;
-  const S* xrow = static_cast<const S*>(p.x) + row * p.ld_x;
-  {
-    Chunk<T> yr[V];
+  const float n_w = wpr == 1 ? (float)C : held(wr);
+  float s = 0.f, m2 = 0.f;
+  if (center) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = (e * wpr + wr) * 32 + lane;
-      chunk_zero(yr[e]);
-      chunk_zero(xr[e]);
-      if (live && c < chunks) {
-        chunk_load(yr[e], yrow + c * 8);
-        chunk_load(xr[e], xrow + c * 8);
-      }
-    }
+    for (int e = 0; e < V; ++e) s += f8_sum(v[e]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) chunk_floats(yr[e], v[e]);
+    for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
-  const float inv_c = 1.0f / (float)p.C;
-  // v := (v - mean) * rstd (RMS norm: mean 0); channels past the row hold zeros before and after.
-  auto normalise = [&](float& mean, float& rstd) {
-    mean = 0.f;
-    if (p.center) {
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s += v[e][j];
-      mean = row_sum(s) * inv_c;
-    }
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if ((e * wpr + wr) * 32 + lane < chunks) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = v[e][j] - mean;
-          ss += d * d;
-        }
-      }
-    rstd = 1.0f / sqrtf(row_sum(ss) * inv_c + p.eps);
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] = (v[e][j] - mean) * rstd;
-  };
-  auto params = [&](const void* ptr, long long off, int c, float (&f)[8]) {
-    Chunk<T> w;
-    chunk_load(w, static_cast<const S*>(ptr) + off + c * 8);
-    chunk_floats(w, f);
-  };
-  float st[4] = {0.f, 0.f, 0.f, 0.f};
-  if (p.post_w) normalise(st[0], st[1]);
-  S* orow = static_cast<S*>(p.x_out) + row * p.ld_x;
-  const long long gate_off = p.gate && live ? row / p.rows_per_gate * p.C : 0;
+  const uint64_t off = f2_same(n_w > 0.f ? -s / n_w : 0.f);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const int c = (e * wpr + wr) * 32 + lane;
-    if (!live || c >= chunks) continue;
-    float f[8], x[8];
-    if (p.post_w) {
-      params(p.post_w, 0, c, f);
+    F8 d;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] *= f[j];
-      if (p.post_b) {
-        params(p.post_b, 0, c, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[e][j] += f[j];
-      }
+    for (int q = 0; q < 4; ++q) {
+      d.p[q] = f2_add(v[e].p[q], off);
+      d.p[q] = f2_mul(d.p[q], d.p[q]);
     }
-    if (p.gate) {
-      params(p.gate, gate_off, c, f);
+    if (chunk(e)) m2 += f8_sum(d);
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] *= f[j];
+  for (int o = LPR / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+  if (wpr > 1) {
+    if ((threadIdx.x & 31) == 0) red[wr] = make_float2(s, m2);
+    meet();
+    s = m2 = 0.f;
+    for (int w = 0; w < wpr; ++w) s += red[w].x;
+    for (int w = 0; w < wpr; ++w) {
+      const float n = held(w);
+      const float2 r = red[w];
+      const float d = center && n > 0.f ? r.x / n - s * inv_c : 0.f;
+      m2 += r.y + n * d * d;
     }
-    if (p.scale) {
-      params(p.scale, 0, c, f);
+  }
+  mean = center ? s * inv_c : 0.f;
+  rstd = rsqrtf(m2 * inv_c + eps);
+}
+
+// The norm and residual arithmetic of one chunk, the same in both kernels.
+struct NormWeights {   // the parameters of a thread's eight channels
+  F8 post_w, post_b, gs, pre_w, pre_b;   // gs = gate * scale
+};
+__device__ __forceinline__ void apply_norm(F8& v, float mean, float rstd, const F8& w, const F8& b) {
+  const uint64_t m = f2_same(-mean), r = f2_same(rstd);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] *= f[j];
-    }
-    chunk_floats(xr[e], x);
+  for (int q = 0; q < 4; ++q)
+    v.p[q] = f2_fma(f2_mul(f2_add(v.p[q], m), r), w.p[q], b.p[q]);
+}
+template <class T>
+__device__ __forceinline__ void load_f8(F8& f, const void* ptr, long long at, float none) {
+  if (!ptr) {
+    f8_fill(f, none);
+    return;
+  }
+  Chunk<T> c;
+  chunk_ldg(c, static_cast<const typename T::Store*>(ptr) + at);
+  f8_unpack(c, f);
+}
+template <class T>
+__device__ __forceinline__ void load_gs(F8& f, const NormParams& p, long long row, int c) {
+  F8 g;
+  load_f8<T>(g, p.gate, p.gate ? row / p.rows_per_gate * p.C + c : 0, 1.f);
+  load_f8<T>(f, p.scale, c, 1.f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[e][j] += x[j];
-    Chunk<T> o;
-    chunk_round(o, v[e]);
-    chunk_store(orow + c * 8, o);
-    chunk_floats(o, v[e]);   // the pre norm is of the stored row
+  for (int q = 0; q < 4; ++q) f.p[q] = f2_mul(f.p[q], g.p[q]);
+}
+
+// Few rows: `wpr` warps a row, one chunk of eight channels a thread, everything loaded at once. What
+// counts is one trip to memory and the two row sums.
+template <class T>
+__global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p, int wpr) {
+  __shared__ float2 red[2][16];
+  using S = typename T::Store;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp % wpr;
+  const int c = (wr * 32 + lane) * 8;
+  const bool col = c < p.C;
+  const long long row = blockIdx.x * (long long)(blockDim.x / 32 / wpr) + warp / wpr;
+  const bool live = col && row < p.rows;
+  griddep_wait();
+  griddep_launch();
+  NormWeights w;
+  F8 v[1], x;
+  f8_fill(v[0], 0.f);
+  f8_fill(x, 0.f);
+  if (live) {
+    Chunk<T> yr, xr;   // (plain loads: the outputs may be these rows)
+    chunk_load(yr, static_cast<const S*>(p.y) + row * p.ld_y + c);
+    chunk_load(xr, static_cast<const S*>(p.x) + row * p.ld_x + c);
+    f8_unpack(yr, v[0]);
+    f8_unpack(xr, x);
+    load_gs<T>(w.gs, p, row, c);
+    load_f8<T>(w.post_w, p.post_w, c, 1.f);
+    load_f8<T>(w.post_b, p.post_b, c, 0.f);
+    load_f8<T>(w.pre_w, p.pre_w, c, 1.f);
+    load_f8<T>(w.pre_b, p.pre_b, c, 0.f);
+  }
+  float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto in_row = [&](int) { return col; };
+  auto meet = [&] { __syncthreads(); };   // the block's rows share its barriers
+  if (p.post_w) {
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+                       st.y);
+    if (live) apply_norm(v[0], st.x, st.y, w.post_w, w.post_b);
+  }
+  if (live) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[0].p[q] = f2_fma(v[0].p[q], w.gs.p[q], x.p[q]);
+    f8_round<T>(v[0], static_cast<S*>(p.x_out) + row * p.ld_x + c);
   }
   if (p.pre_w) {
-    // Channels past the row must not count: they hold -mean * rstd of the post norm.
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (!live || (e * wpr + wr) * 32 + lane >= chunks) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[e][j] = 0.f;
-      }
-    normalise(st[2], st[3]);
-    S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int c = (e * wpr + wr) * 32 + lane;
-      if (!live || c >= chunks) continue;
-      float f[8];
-      params(p.pre_w, 0, c, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[e][j] *= f[j];
-      if (p.pre_b) {
-        params(p.pre_b, 0, c, f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[e][j] += f[j];
-      }
-      Chunk<T> o;
-      chunk_round(o, v[e]);
-      chunk_store(nrow + c * 8, o);
+    if (!live) f8_fill(v[0], 0.f);
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+                       st.w);
+    if (live) {
+      apply_norm(v[0], st.z, st.w, w.pre_w, w.pre_b);
+      f8_store<T>(static_cast<S*>(p.n) + row * p.ld_n + c, v[0]);
     }
   }
-  if (p.stats && live && wr == 0 && lane == 0)
-    reinterpret_cast<float4*>(p.stats)[row] = make_float4(st[0], st[1], st[2], st[3]);
+  if (p.stats && live && c == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
 }
 
-template <class T, int V>
-static cudaError_t launch_fwd(const NormParams& p, int wpr, cudaStream_t st) {
-  const int rpb = 8 / wpr;
-  return launch_pdl(k_norm_residual<T, V>, dim3((unsigned)((p.rows + rpb - 1) / rpb)), dim3(256), 0,
-                    st, p, wpr);
+// Many rows: a persistent CTA of 24 warps an SM; `wpr` warps hold a row, each a span of it with V chunks
+// of eight channels a lane, so that a row's sums cost a few shuffles per V chunks and nothing waits for
+// another warp at wpr == 1. Every warp has a slot of shared memory for its y and one for its x, which
+// bulk copies fill with the next row's as soon as this one's values are read: the memory stays busy
+// without registers for it, and 80 registers a thread leave room for the 24 warps that hide the sums'
+// latency. The parameters sit in shared memory in fp32 (scale folded into the post norm's); the gate,
+// which changes with the row, is read from L1. LPR < 32: narrow rows, 32 / LPR of them a warp. FULL: every
+// lane's V chunks are in the row.
+constexpr int kFwdWarps = 24, kFwdThreads = 32 * kFwdWarps;
+
+template <class T, int V, int LPR, bool FULL>
+__global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormParams p, int wpr,
+                                                                  int* status) {
+  using S = typename T::Store;
+  constexpr int kRows = 32 / LPR;                   // rows a warp holds
+  constexpr int kSlot = kRows * V * LPR * 8;        // elements of a warp's y or x
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[2][kFwdWarps];
+  __shared__ float2 red[2][kFwdWarps];
+  __shared__ int abort_flag;
+  S* slots = reinterpret_cast<S*>(smem);            // [warps][y, x][kSlot]
+  float* prm = reinterpret_cast<float*>(smem + 2 * kFwdWarps * kSlot * sizeof(S));
+  // prm [4][C]: scale * post_w, scale * post_b, pre_w, pre_b
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wr = warp % wpr, C = p.C;
+  if (threadIdx.x < 2 * kFwdWarps) mbar_init(&full[0][0] + threadIdx.x, 1);
+  if (threadIdx.x == 0) abort_flag = 0;
+  fence_barrier_init();
+  __syncthreads();
+  griddep_wait();
+  griddep_launch();
+
+  const int per_cta = kFwdWarps / wpr * kRows;
+  const long long stride = (long long)gridDim.x * per_cta;
+  const long long first = (long long)blockIdx.x * per_cta + warp / wpr * kRows;   // of the warp
+  const int c0 = wr * V * LPR * 8;                  // first channel of the warp's span
+  const int span = FULL || C - c0 > V * LPR * 8 ? V * LPR * 8 : C > c0 ? C - c0 : 0;
+  S* slot_y = slots + (size_t)warp * 2 * kSlot;
+  S* slot_x = slot_y + kSlot;
+  // The warp's span of its rows from `row` on (rows kSlot / kRows apart in the slot).
+  auto fetch = [&](S* to, const void* src, long long ld, long long row, uint64_t* bar) {
+    const int n = (int)(p.rows - row < kRows ? p.rows - row : kRows);
+    mbar_expect_tx(bar, (uint32_t)(n * span * (int)sizeof(S)));
+    if (span > 0)
+      for (int i = 0; i < n; ++i)
+        bulk_load(to + i * (kSlot / kRows), static_cast<const S*>(src) + (row + i) * ld + c0,
+                  (uint32_t)(span * (int)sizeof(S)), bar);
+  };
+  if (lane == 0 && first < p.rows) {
+    fetch(slot_y, p.y, p.ld_y, first, &full[0][warp]);
+    fetch(slot_x, p.x, p.ld_x, first, &full[1][warp]);
+  }
+  for (int c = threadIdx.x * 8; c < C; c += kFwdThreads * 8) {
+    F8 a, b, k;
+    load_f8<T>(k, p.scale, c, 1.f);
+    load_f8<T>(a, p.post_w, c, 1.f);
+    load_f8<T>(b, p.post_b, c, 0.f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      a.p[q] = f2_mul(a.p[q], k.p[q]);
+      b.p[q] = f2_mul(b.p[q], k.p[q]);
+    }
+    f8_put(prm, C, c, a);
+    f8_put(prm + C, C, c, b);
+    load_f8<T>(a, p.pre_w, c, 1.f);
+    load_f8<T>(b, p.pre_b, c, 0.f);
+    f8_put(prm + 2 * C, C, c, a);
+    f8_put(prm + 3 * C, C, c, b);
+  }
+  __syncthreads();
+  const int l = lane % LPR, sub = lane / LPR;
+  const int mine = sub * (kSlot / kRows) + l * 8;    // in a slot; chunk e is LPR * 8 further on
+  const int cl = c0 + l * 8;                        // the lane's first channel
+  auto in_row = [&](int e) { return FULL || l * 8 + e * LPR * 8 < span; };
+  auto meet = [&] { named_barrier(1 + warp / wpr, wpr * 32); };
+  int phase = 0;
+  for (long long at = first; at < p.rows; at += stride, phase ^= 1) {
+    const long long row = at + sub;
+    const bool live = LPR == 32 || row < p.rows;
+    F8 v[V];
+    // A wait that gives up is recorded; the walk goes on to its end, so that no barrier is left with
+    // missing threads (the addresses do not depend on the data).
+    mbar_wait(&full[0][warp], phase, &abort_flag, status);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      f8_fill(v[e], 0.f);
+      if (live && in_row(e)) {
+        Chunk<T> t;
+        chunk_load(t, slot_y + mine + e * LPR * 8);
+        f8_unpack(t, v[e]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0 && at + stride < p.rows)
+      fetch(slot_y, p.y, p.ld_y, at + stride, &full[0][warp]);
+    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.post_w)
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+                          st.y);
+    const uint64_t rs = f2_same(p.post_w ? st.y : 1.f), ms = f2_same(-st.x * st.y);
+    const S* gate = static_cast<const S*>(p.gate);
+    if (gate && live) gate += row / p.rows_per_gate * C;
+    S* out = static_cast<S*>(p.x_out) + row * p.ld_x;
+    mbar_wait(&full[1][warp], phase, &abort_flag, status);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      // (one chunk's operands at a time: gathering them ahead would cost the registers)
+      asm volatile("" ::: "memory");
+      if (!live || !in_row(e)) {
+        f8_fill(v[e], 0.f);
+        continue;
+      }
+      const int c = cl + e * LPR * 8;
+      F8 w, b, x;
+      Chunk<T> t;
+      chunk_load(t, slot_x + mine + e * LPR * 8);
+      f8_unpack(t, x);
+      f8_get(w, prm, C, c);
+      f8_get(b, prm + C, C, c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[e].p[q] = f2_fma(f2_fma(v[e].p[q], rs, ms), w.p[q], b.p[q]);
+      if (gate) {
+        load_f8<T>(w, gate, c, 1.f);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[e].p[q] = f2_fma(v[e].p[q], w.p[q], x.p[q]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[e].p[q] = f2_add(v[e].p[q], x.p[q]);
+      }
+      f8_round<T>(v[e], out + c);
+    }
+    __syncwarp();
+    if (lane == 0 && at + stride < p.rows)
+      fetch(slot_x, p.x, p.ld_x, at + stride, &full[1][warp]);
+    if (p.pre_w) {
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+                          st.w);
+      const uint64_t r2 = f2_same(st.w), m2 = f2_same(-st.z * st.w);
+      S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        asm volatile("" ::: "memory");
+        if (!live || !in_row(e)) continue;
+        const int c = cl + e * LPR * 8;
+        F8 w, b;
+        f8_get(w, prm + 2 * C, C, c);
+        f8_get(b, prm + 3 * C, C, c);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[e].p[q] = f2_fma(f2_fma(v[e].p[q], r2, m2), w.p[q], b.p[q]);
+        f8_store<T>(nrow + c, v[e]);
+      }
+    }
+    if (p.stats && live && wr == 0 && l == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
+    // One norm only: its next meeting must not overtake a warp that still reads this one's sums.
+    if (wpr > 1 && (p.post_w == nullptr) != (p.pre_w == nullptr)) meet();
+  }
 }
 
-cudaError_t launch_norm_residual(const NormParams& p, int dtype, cudaStream_t st) {
-  // The fewest warps a row with at most five chunks a lane (40 fp32 values, C = 1280 in one warp).
-  const int chunks = p.C / 8;
-  int wpr = 1;
-  while (wpr < 8 && chunks > 32 * 5 * wpr) wpr *= 2;
-  const int v = (chunks + 32 * wpr - 1) / (32 * wpr);
+// ---- shared by the persistent backward ------------------------------------------------------
+constexpr int kNormThreads = 512;
+constexpr int kNormRingBytes = 184 * 1024;
+constexpr int kNormMaxStages = 4;
+
+struct NormShape {
+  long long rows_per_worker;
+  int workers, wpg, rl;     // workers in all; warps per worker; workers per CTA
+  int stages, stage_bytes;  // ring of one worker
+};
+
+// The workers' geometry for `tensors` rows of C channels a stage and R rows at a time, plus `extra` bytes a row.
+static NormShape norm_shape(long long rows, int C, int es, int tensors, int R, int extra) {
+  NormShape g;
+  g.wpg = (C / 8 + 31) / 32;
+  g.rl = (kNormThreads / 32) / g.wpg;
+  g.stage_bytes = R * (tensors * C * es + extra);
+  while (g.rl > 1 && kNormRingBytes / (g.rl * g.stage_bytes) < 2) --g.rl;
+  g.stages = kNormRingBytes / (g.rl * g.stage_bytes);
+  if (g.stages > kNormMaxStages) g.stages = kNormMaxStages;
+  const long long most = (long long)kNormMaxCtas * g.rl;
+  g.rows_per_worker = (rows + most - 1) / most;
+  if (g.rows_per_worker < 1) g.rows_per_worker = 1;
+  g.workers = (int)((rows + g.rows_per_worker - 1) / g.rows_per_worker);
+  return g;
+}
+
+template <class T, int V, int LPR>
+static cudaError_t launch_fwd(const NormParams& p, int wpr, int* status, cudaStream_t st) {
+  const auto kernel = p.C == V * LPR * wpr * 8 ? k_norm_residual<T, V, LPR, true>
+                                               : k_norm_residual<T, V, LPR, false>;
+  const size_t smem = (size_t)2 * kFwdWarps * V * 32 * 8 * sizeof(typename T::Store) +
+                      (size_t)4 * p.C * sizeof(float);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int per_cta = kFwdWarps / wpr * (32 / LPR);
+  const long long ctas = (p.rows + per_cta - 1) / per_cta;
+  return launch_pdl(kernel, dim3((unsigned)(ctas < kNormMaxCtas ? ctas : kNormMaxCtas)),
+                    dim3(kFwdThreads), smem, st, p, wpr, status);
+}
+
+cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cudaStream_t st) {
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    switch (v) {
-      case 1: return launch_fwd<T, 1>(p, wpr, st);
-      case 2: return launch_fwd<T, 2>(p, wpr, st);
-      case 3: return launch_fwd<T, 3>(p, wpr, st);
-      case 4: return launch_fwd<T, 4>(p, wpr, st);
-      default: return launch_fwd<T, 5>(p, wpr, st);
+    const int chunks = p.C / 8;
+    if (p.rows <= kNormDirectRows) {
+      int wpr = 1;
+      while (wpr * 32 < chunks) wpr *= 2;
+      const int rpb = wpr < 4 ? 4 / wpr : 1;
+      return launch_pdl(k_norm_residual_direct<T>, dim3((unsigned)((p.rows + rpb - 1) / rpb)),
+                        dim3(wpr * rpb * 32), 0, st, p, wpr);
+    }
+    if (chunks <= 8) return launch_fwd<T, 1, 8>(p, 1, status, st);
+    if (chunks <= 16) return launch_fwd<T, 1, 16>(p, 1, status, st);
+    // The fewest warps a row with at most 40 values a lane (fp32: 24, for the slots' size).
+    constexpr int kMost = T::kWords == 8 ? 3 : 5;
+    int wpr = 1;
+    while (chunks > 32 * kMost * wpr) wpr *= 2;
+    switch ((chunks + 32 * wpr - 1) / (32 * wpr)) {
+      case 1: return launch_fwd<T, 1, 32>(p, wpr, status, st);
+      case 2: return launch_fwd<T, 2, 32>(p, wpr, status, st);
+      case 3: return launch_fwd<T, 3, 32>(p, wpr, status, st);
+      case 4: return launch_fwd<T, kMost < 4 ? 3 : 4, 32>(p, wpr, status, st);
+      default: return launch_fwd<T, kMost < 5 ? 3 : 5, 32>(p, wpr, status, st);
     }
   });
 }
@@ -199,36 +453,26 @@ cudaError_t launch_norm_residual(const NormParams& p, int dtype, cudaStream_t st
 // so four fp32 accumulators a channel serve all six.
 //
 // A worker is a group of `wpg` warps (one chunk of eight channels a thread) that walks its own
-// contiguous rows, R at a time: bulk copies bring the rows of all four inputs into the worker's ring
-// of shared-memory stages, well ahead of use, so that the row sums' barriers do not idle the memory.
+// contiguous rows, R at a time (two rows share the row sums' meetings): bulk copies bring the rows of
+// all inputs, with their statistics, into the worker's ring of shared-memory stages ahead of use.
 // Several workers share a CTA (one per SM); at the end their column sums are added in worker order
 // and written as one partial per CTA, which k_norm_reduce adds in CTA order: no atomics, the same
 // result every run.
-constexpr int kNormThreads = 512;
-constexpr int kNormRingBytes = 192 * 1024;
-constexpr int kNormMaxStages = 4;
-
-struct NormBwdShape {
-  long long rows_per_worker;
-  int workers, wpg, rl;     // workers in all; warps per worker; workers per CTA
-  int stages, stage_bytes;  // ring of one worker
-  int tensors;              // rows brought per stage: dx_out, y, then x and dn with a pre norm
-};
-
-template <class T, int R>
+template <class T, int R, bool PRE, bool POST>
 __global__ void __launch_bounds__(kNormThreads, 1)
-    k_norm_residual_backward(const NormBwdParams p, const NormBwdShape g, int* status) {
+    k_norm_residual_backward(const NormBwdParams p, const NormShape g, int* status) {
   using S = typename T::Store;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[16 * kNormMaxStages];
-  __shared__ float red[2][16][2 * R];   // [buffer][warp][sums]
+  __shared__ float2 red[2][16][R];   // [buffer][warp][row]
   __shared__ int abort_flag;
+  constexpr int kTensors = PRE ? 4 : 2;
+  constexpr bool kStats = PRE || POST;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rl = warp / g.wpg, wg = warp % g.wpg;
-  const int tw = wg * 32 + lane;            // thread in the worker
+  const int tw = wg * 32 + lane, c = tw * 8;
   const int worker = blockIdx.x * g.rl + rl;
-  const int chunks = p.C / 8;
-  const bool col = tw < chunks && rl < g.rl;
+  const bool col = c < p.C && rl < g.rl;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.rl * g.stages; ++i) mbar_init(full + i, 1);
     abort_flag = 0;
@@ -242,268 +486,326 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   long long r1 = r0 + g.rows_per_worker;
   if (r1 > p.rows) r1 = p.rows;
   uint8_t* ring = smem + (size_t)rl * g.stages * g.stage_bytes;
+  // P1 and P0 of the worker's closed groups (with a gate): [2][C] behind the rings.
+  float* closed = reinterpret_cast<float*>(smem + (size_t)g.rl * g.stages * g.stage_bytes) +
+                  (size_t)rl * 2 * p.C + c;
   uint64_t* bar = full + rl * g.stages;
   const int row_bytes = p.C * (int)sizeof(S);
-  // Batches never cross a group of rows that share a gate row.
-  auto batch_rows = [&](long long r) {
-    long long e = r1;
-    if (p.gate) {
-      const long long ge = (r / p.rows_per_gate + 1) * p.rows_per_gate;
-      if (ge < e) e = ge;
-    }
-    return (int)(e - r < R ? e - r : R);
-  };
-  const void* src[4] = {p.dx_out, p.y, p.x, p.dn};
-  const long long ld[4] = {p.ld_x, p.ld_y, p.ld_x, p.ld_n};
+  const bool dense = p.ld_x == p.C && p.ld_y == p.C && p.ld_n == p.C;
+  // Up to R rows from r into stage st: [R stats][dx_out rows][y][x_out][dn].
   auto fetch = [&](long long r, int st) {
-    const int n = batch_rows(r);
-    mbar_expect_tx(bar + st, (uint32_t)(g.tensors * n * row_bytes));
-    for (int t = 0; t < g.tensors; ++t)
-      for (int i = 0; i < n; ++i)
-        bulk_load(ring + (size_t)st * g.stage_bytes + (size_t)(t * R + i) * row_bytes,
-                  static_cast<const S*>(src[t]) + (r + i) * ld[t], (uint32_t)row_bytes, bar + st);
-    return r + n;
+    const int n = (int)(r1 - r < R ? r1 - r : R);
+    uint8_t* to = ring + (size_t)st * g.stage_bytes;
+    mbar_expect_tx(bar + st, (uint32_t)(n * (kTensors * row_bytes + (kStats ? 16 : 0))));
+    if (kStats) bulk_load(to, p.stats + r * 4, (uint32_t)n * 16, bar + st);
+    to += R * 16;
+    auto rows = [&](const void* src, long long ld) {
+      const S* from = static_cast<const S*>(src) + r * ld;
+      if (dense) {
+        bulk_load(to, from, (uint32_t)(n * row_bytes), bar + st);
+      } else {
+        for (int i = 0; i < n; ++i)
+          bulk_load(to + i * row_bytes, from + i * ld, (uint32_t)row_bytes, bar + st);
+      }
+      to += R * row_bytes;
+    };
+    rows(p.dx_out, p.ld_x);
+    rows(p.y, p.ld_y);
+    if (PRE) {
+      rows(p.x, p.ld_x);
+      rows(p.dn, p.ld_n);
+    }
   };
   long long ahead = r0;
   if (rl < g.rl && tw == 0)
-    for (int s = 0; s < g.stages && ahead < r1; ++s) ahead = fetch(ahead, s);
+    for (int s = 0; s < g.stages && ahead < r1; ++s, ahead += R) fetch(ahead, s);
 
-  auto params = [&](const void* ptr, long long off, float (&f)[8]) {
-    Chunk<T> w;
-    chunk_load(w, static_cast<const S*>(ptr) + off + tw * 8);
-    chunk_floats(w, f);
+  F8 w_pre, coef;                       // coef = gate * scale * post_w
+  F8 acc_pw, acc_pb, acc_a, acc_b;
+  f8_fill(w_pre, 0.f);
+  f8_fill(coef, 0.f);
+  f8_fill(acc_pw, 0.f);
+  f8_fill(acc_pb, 0.f);
+  f8_fill(acc_a, 0.f);
+  f8_fill(acc_b, 0.f);
+  auto load_coef = [&](long long group) {
+    F8 f;
+    load_f8<T>(coef, p.post_w, c, 1.f);
+    load_f8<T>(f, p.scale, c, 1.f);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) coef.p[q] = f2_mul(coef.p[q], f.p[q]);
+    if (p.gate) {
+      load_f8<T>(f, p.gate, group * p.C + c, 1.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) coef.p[q] = f2_mul(coef.p[q], f.p[q]);
+    }
   };
-  const bool pre = p.pre_w != nullptr, post = p.post_w != nullptr;
-  float wpre[8], coef[8], base[8];   // base = scale * post_w; coef = gate * base
-  float acc_pw[8], acc_pb[8], acc_a[8], acc_b[8], tot_a[8], tot_b[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    wpre[j] = 0.f;
-    base[j] = 1.f;
-    acc_pw[j] = acc_pb[j] = acc_a[j] = acc_b[j] = tot_a[j] = tot_b[j] = 0.f;
-  }
   if (col) {
-    float f[8];
-    if (pre) params(p.pre_w, 0, wpre);
-    if (p.scale) {
-      params(p.scale, 0, base);
-    }
-    if (post) {
-      params(p.post_w, 0, f);
+    if (PRE) load_f8<T>(w_pre, p.pre_w, c, 1.f);
+    if (!p.gate) load_coef(0);
+    if (p.gate) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) base[j] *= f[j];
+      for (int j = 0; j < 8; ++j) closed[j] = closed[p.C + j] = 0.f;
     }
   }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) coef[j] = base[j];
-
-  // The sums of 2 R values over the worker's threads.
+  auto meet = [&] {
+    if (g.wpg > 1) named_barrier(1 + rl, g.wpg * 32);
+    else __syncwarp();
+  };
+  // (a, b) of each row summed over the worker's threads: after the first exchange the two halves of a
+  // warp carry one sum each (two rows: after the second, the quarters), so that R rows cost five or
+  // six shuffles.
   int buf = 0;
-  auto worker_sums = [&](float (&s)[2 * R]) {
+  auto worker_sums = [&](float (&a)[R], float (&b)[R], auto&& met) {
+    const bool hi = lane & 16;
+    float v;
+    if constexpr (R == 1) {
+      v = hi ? b[0] : a[0];
+      v += __shfl_xor_sync(0xffffffffu, hi ? a[0] : b[0], 16);
 #pragma unroll
-    for (int i = 0; i < 2 * R; ++i) s[i] = warp_sum(s[i]);
+      for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+      float v0 = hi ? b[0] : a[0], v1 = hi ? b[1] : a[1];
+      v0 += __shfl_xor_sync(0xffffffffu, hi ? a[0] : b[0], 16);
+      v1 += __shfl_xor_sync(0xffffffffu, hi ? a[1] : b[1], 16);
+      const bool second = lane & 8;
+      v = second ? v1 : v0;
+      v += __shfl_xor_sync(0xffffffffu, second ? v0 : v1, 8);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    // lane 16 h + 8 i holds row i's sum h
     if (g.wpg > 1) {
-      if (lane == 0) {
+      float* mine = reinterpret_cast<float*>(&red[buf][warp][0]);
+      if ((lane & (R == 1 ? 15 : 7)) == 0) mine[R == 1 ? lane >> 4 : ((lane >> 2) & 2) + (lane >> 4)] = v;
+      met();
 #pragma unroll
-        for (int i = 0; i < 2 * R; ++i) red[buf][warp][i] = s[i];
+      for (int i = 0; i < R; ++i) a[i] = b[i] = 0.f;
+#pragma unroll 4
+      for (int w = 0; w < g.wpg; ++w) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          const float2 e = red[buf][warp - wg + w][i];
+          a[i] += e.x;
+          b[i] += e.y;
+        }
       }
-      named_barrier(1 + rl, g.wpg * 32);
-#pragma unroll
-      for (int i = 0; i < 2 * R; ++i) s[i] = 0.f;
-      for (int w = 0; w < g.wpg; ++w)
-#pragma unroll
-        for (int i = 0; i < 2 * R; ++i) s[i] += red[buf][warp - wg + w][i];
       buf ^= 1;
+    } else {
+      met();
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        a[i] = __shfl_sync(0xffffffffu, v, 8 * i);
+        b[i] = __shfl_sync(0xffffffffu, v, 16 + 8 * i);
+      }
     }
   };
   const float inv_c = 1.0f / (float)p.C;
-  const float mean_on = p.center ? 1.f : 0.f;
-  long long group = -1;
-  int it = 0;
+  const float mean_on = p.center ? inv_c : 0.f;
+  long long group = -1, group_end = p.gate ? 0 : p.rows;
   // The gate row of the finished group: final if all its rows were this worker's, else a partial in
   // the worker's first slot (its first group) or second.
   auto close_group = [&]() {
-    if (!p.gate || group < 0 || !col) return;
+    if (group < 0 || !col) return;
     const long long g0 = group * p.rows_per_gate;
-    long long g1 = g0 + p.rows_per_gate;
-    if (g1 > p.rows) g1 = p.rows;
-    const bool whole = g0 >= r0 && g1 <= r1;
-    float gate[8], f[8], dg[8];
-    params(p.gate, group * p.C, gate);
+    const bool whole = g0 >= r0 && (group_end <= r1 || r1 == p.rows);
+    float a[8], b[8], f[8], dg[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = 1.f;
-    if (post) params(p.post_w, 0, f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dg[j] = f[j] * acc_a[j];
-    if (p.post_b) {
-      params(p.post_b, 0, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) dg[j] += f[j] * acc_b[j];
+    for (int q = 0; q < 4; ++q) {
+      f2_unpack(acc_a.p[q], a[2 * q], a[2 * q + 1]);
+      f2_unpack(acc_b.p[q], b[2 * q], b[2 * q + 1]);
     }
-    if (p.scale) {
-      params(p.scale, 0, f);
+    auto floats = [&](const void* ptr, long long at, float none) {
+      F8 t;
+      load_f8<T>(t, ptr, at, none);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dg[j] *= f[j];
-    }
-    float* out = whole ? p.dgate + group * p.C
-                       : p.gate_partial + ((long long)worker * 2 + (g0 > r0 ? 1 : 0)) * p.C;
+      for (int q = 0; q < 4; ++q) f2_unpack(t.p[q], f[2 * q], f[2 * q + 1]);
+    };
+    floats(p.post_w, c, 1.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] = f[j] * a[j];
+    floats(p.post_b, c, 0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] += f[j] * b[j];
+    floats(p.scale, c, 1.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dg[j] *= f[j];
     if (!whole || p.dgate) {
-#pragma unroll
-      for (int j = 0; j < 8; j += 4)
-        reinterpret_cast<float4*>(out + tw * 8 + j)[0] =
-            make_float4(dg[j], dg[j + 1], dg[j + 2], dg[j + 3]);
+      float* out = whole ? p.dgate + group * p.C + c
+                         : p.gate_partial + ((long long)worker * 2 + (g0 > r0 ? 1 : 0)) * p.C + c;
+      reinterpret_cast<float4*>(out)[0] = make_float4(dg[0], dg[1], dg[2], dg[3]);
+      reinterpret_cast<float4*>(out)[1] = make_float4(dg[4], dg[5], dg[6], dg[7]);
     }
+    floats(p.gate, group * p.C + c, 1.f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      tot_a[j] += gate[j] * acc_a[j];
-      tot_b[j] += gate[j] * acc_b[j];
-      acc_a[j] = acc_b[j] = 0.f;
+      closed[j] += f[j] * a[j];
+      closed[p.C + j] += f[j] * b[j];
     }
+    f8_fill(acc_a, 0.f);
+    f8_fill(acc_b, 0.f);
+  };
+  S* dx = static_cast<S*>(p.dx) + r0 * p.ld_x + c;
+  S* dy = static_cast<S*>(p.dy) + r0 * p.ld_y + c;
+  // One step: rows r .. r + n - 1 (n <= R), at rows `at`.. of stage st; `last`: nothing of the stage is
+  // needed after it.
+  auto step = [&](int n, int at, int st, bool last) {
+    const uint8_t* sp = ring + (size_t)st * g.stage_bytes;
+    const float4* stat = reinterpret_cast<const float4*>(sp) + at;
+    const S* rows = reinterpret_cast<const S*>(sp + R * 16) + at * p.C + c;
+    const int next = R * p.C;   // from one input's rows to the next's
+    bool live[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) live[i] = col && (R == 1 || i < n);
+    auto read = [&](F8& f, int which, int i) {
+      Chunk<T> t;
+      if (live[i]) chunk_load(t, rows + which * next + i * p.C);
+      else chunk_zero(t);
+      f8_unpack(t, f);
+    };
+    // The last meeting of the worker's warps also frees the stage: every thread has its chunks.
+    auto release = [&] {
+      meet();
+      if (last && tw == 0 && ahead < r1) {
+        fetch(ahead, st);
+        ahead += R;
+      }
+    };
+    F8 D[R], h[R];
+    float a[R], b[R];
+    if constexpr (PRE) {
+      F8 dn[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        read(h[i], 2, i);
+        read(dn[i], 3, i);
+        // (an absent row's statistics are whatever the stage held: not to be multiplied by 0)
+        const float2 t = R == 1 || i < n ? reinterpret_cast<const float2*>(stat + i)[1]
+                                         : make_float2(0.f, 0.f);
+        const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
+        F8 s1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
+          acc_pw.p[q] = f2_fma(dn[i].p[q], h[i].p[q], acc_pw.p[q]);
+          acc_pb.p[q] = f2_add(acc_pb.p[q], dn[i].p[q]);
+          dn[i].p[q] = f2_mul(dn[i].p[q], w_pre.p[q]);
+          s1.p[q] = f2_mul(dn[i].p[q], h[i].p[q]);
+        }
+        a[i] = f8_sum(dn[i]);
+        b[i] = f8_sum(s1);
+      }
+      worker_sums(a, b, meet);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        read(D[i], 0, i);
+        const float r = R == 1 || i < n ? stat[i].w : 0.f;
+        const uint64_t rs = f2_same(r);
+        const uint64_t k0 = f2_same(-r * (a[i] * mean_on)), k1 = f2_same(-r * (b[i] * inv_c));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          D[i].p[q] = f2_add(D[i].p[q], f2_fma(dn[i].p[q], rs, f2_fma(h[i].p[q], k1, k0)));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) read(D[i], 0, i);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      // h_post (or y), the column sums and, with a post norm, the row sums.
+      read(h[i], 1, i);
+      if (live[i]) f8_store<T>(dx + i * p.ld_x, D[i]);
+      if constexpr (POST) {
+        const float2 t = R == 1 || i < n ? *reinterpret_cast<const float2*>(stat + i)
+                                         : make_float2(0.f, 0.f);
+        const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        acc_a.p[q] = f2_fma(D[i].p[q], h[i].p[q], acc_a.p[q]);
+        acc_b.p[q] = f2_add(acc_b.p[q], D[i].p[q]);
+        D[i].p[q] = f2_mul(D[i].p[q], coef.p[q]);
+      }
+      if constexpr (POST) {
+        F8 s1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s1.p[q] = f2_mul(D[i].p[q], h[i].p[q]);
+        a[i] = f8_sum(D[i]);
+        b[i] = f8_sum(s1);
+      }
+    }
+    if constexpr (POST) {
+      float rstd[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) rstd[i] = R == 1 || i < n ? stat[i].y : 0.f;
+      worker_sums(a, b, release);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const uint64_t rs = f2_same(rstd[i]);
+        const uint64_t k0 = f2_same(-rstd[i] * (a[i] * mean_on));
+        const uint64_t k1 = f2_same(-rstd[i] * (b[i] * inv_c));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          D[i].p[q] = f2_fma(D[i].p[q], rs, f2_fma(h[i].p[q], k1, k0));
+      }
+    }
+    if constexpr (!POST) release();
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (live[i]) f8_store<T>(dy + i * p.ld_y, D[i]);
+    dx += n * p.ld_x;
+    dy += n * p.ld_y;
   };
   if (rl < g.rl) {
-    for (long long r = r0; r < r1; ++it) {
-      const int n = batch_rows(r);
-      const int st = it % g.stages;
-      if (p.gate) {
-        const long long gr = r / p.rows_per_gate;
-        if (gr != group) {
-          close_group();
-          group = gr;
-          if (col) {
-            float f[8];
-            params(p.gate, group * p.C, f);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) coef[j] = base[j] * f[j];
-          }
-        }
-      }
+    int st = 0, phase = 0;
+    for (long long r = r0; r < r1; r += R) {
+      const int n = (int)(r1 - r < R ? r1 - r : R);
       // A wait that gives up is recorded; the walk goes on to its end, so that no barrier is left
       // with missing threads (the addresses do not depend on the data).
-      mbar_wait(bar + st, (it / g.stages) & 1, &abort_flag, status);
-      Chunk<T> c_d[R], c_y[R], c_x[R], c_n[R];
-      float4 stat[R];
-      const uint8_t* sp = ring + (size_t)st * g.stage_bytes + (size_t)tw * 8 * sizeof(S);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        chunk_zero(c_d[i]);
-        chunk_zero(c_y[i]);
-        chunk_zero(c_x[i]);
-        chunk_zero(c_n[i]);
-        stat[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (col && i < n) {
-          const size_t ro = (size_t)i * row_bytes;
-          const size_t to = (size_t)R * row_bytes;
-          chunk_load(c_d[i], reinterpret_cast<const S*>(sp + ro));
-          chunk_load(c_y[i], reinterpret_cast<const S*>(sp + to + ro));
-          if (pre) {
-            chunk_load(c_x[i], reinterpret_cast<const S*>(sp + 2 * to + ro));
-            chunk_load(c_n[i], reinterpret_cast<const S*>(sp + 3 * to + ro));
-          }
-          stat[i] = __ldg(reinterpret_cast<const float4*>(p.stats) + r + i);
+      mbar_wait(bar + st, phase, &abort_flag, status);
+      // Rows of one step share a gate row: a stage with a border between its rows takes a step each.
+      int done = 0;
+      do {
+        const long long at = r + done;
+        if (at >= group_end) {
+          close_group();
+          group = at / p.rows_per_gate;
+          group_end = (group + 1) * p.rows_per_gate;
+          if (col) load_coef(group);
         }
+        const int m = (int)(group_end - at < n - done ? group_end - at : n - done);
+        step(m, done, st, done + m == n);
+        done += m;
+      } while (done < n);
+      if (++st == g.stages) {
+        st = 0;
+        phase ^= 1;
       }
-      // Every thread has its chunks: the stage can be filled again.
-      if (g.wpg > 1) named_barrier(1 + rl, g.wpg * 32);
-      else __syncwarp();
-      if (tw == 0 && ahead < r1) ahead = fetch(ahead, st);
-      float D[R][8];
-#pragma unroll
-      for (int i = 0; i < R; ++i) chunk_floats(c_d[i], D[i]);
-      if (pre) {
-        float s[2 * R];
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          float x[8], dn[8];
-          chunk_floats(c_x[i], x);
-          chunk_floats(c_n[i], dn);
-          s[2 * i] = s[2 * i + 1] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float h = (x[j] - stat[i].z) * stat[i].w;
-            const float gg = dn[j] * wpre[j];
-            s[2 * i] += gg;
-            s[2 * i + 1] += gg * h;
-            acc_pw[j] += dn[j] * h;
-            acc_pb[j] += dn[j];
-          }
-        }
-        worker_sums(s);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-          float x[8], dn[8];
-          chunk_floats(c_x[i], x);
-          chunk_floats(c_n[i], dn);
-          const float m0 = s[2 * i] * inv_c * mean_on, m1 = s[2 * i + 1] * inv_c;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float h = (x[j] - stat[i].z) * stat[i].w;
-            D[i][j] += stat[i].w * (dn[j] * wpre[j] - m0 - h * m1);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (col && i < n) {
-          Chunk<T> o;
-          chunk_round(o, D[i]);
-          chunk_store(static_cast<S*>(p.dx) + (r + i) * p.ld_x + tw * 8, o);
-        }
-      // h_post (or y), the column sums and, with a post norm, the row sums.
-      float s[2 * R];
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        float y[8];
-        chunk_floats(c_y[i], y);
-        s[2 * i] = s[2 * i + 1] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float h = post ? (y[j] - stat[i].x) * stat[i].y : y[j];
-          acc_a[j] += D[i][j] * h;
-          acc_b[j] += D[i][j];
-          const float q = D[i][j] * coef[j];
-          s[2 * i] += q;
-          s[2 * i + 1] += q * h;
-        }
-      }
-      if (post) worker_sums(s);
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (!col || i >= n) continue;
-        float y[8], o8[8];
-        chunk_floats(c_y[i], y);
-        const float m0 = s[2 * i] * inv_c * mean_on, m1 = s[2 * i + 1] * inv_c;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float q = D[i][j] * coef[j];
-          o8[j] = post ? stat[i].y * (q - m0 - (y[j] - stat[i].x) * stat[i].y * m1) : q;
-        }
-        Chunk<T> o;
-        chunk_round(o, o8);
-        chunk_store(static_cast<S*>(p.dy) + (r + i) * p.ld_y + tw * 8, o);
-      }
-      r += n;
     }
-    close_group();
+    if (p.gate) close_group();
   }
-  if (!p.gate) {
+  // The CTA's column sums, in worker order: [pre_w, pre_b, P1, P0][C]. The rings are free now: every
+  // copy into them has been waited for (the closed groups' sums are read before they are overwritten).
+  F8 p1 = acc_a, p0 = acc_b;
+  if (p.gate && col) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      tot_a[j] = acc_a[j];
-      tot_b[j] = acc_b[j];
+    for (int q = 0; q < 4; ++q) {
+      p1.p[q] = f2_pack(closed[2 * q], closed[2 * q + 1]);
+      p0.p[q] = f2_pack(closed[p.C + 2 * q], closed[p.C + 2 * q + 1]);
     }
   }
-  // The CTA's column sums, in worker order: [pre_w, pre_b, P1, P0][C]. The ring is free now: every
-  // copy into it has been waited for.
   __syncthreads();
   float* sums = reinterpret_cast<float*>(smem);
   if (col) {
-    float* mine = sums + (size_t)rl * 4 * p.C + tw * 8;
+    float* mine = sums + (size_t)rl * 4 * p.C + c;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      mine[j] = acc_pw[j];
-      mine[p.C + j] = acc_pb[j];
-      mine[2 * p.C + j] = tot_a[j];
-      mine[3 * p.C + j] = tot_b[j];
+    for (int q = 0; q < 4; ++q) {
+      f2_unpack(acc_pw.p[q], mine[2 * q], mine[2 * q + 1]);
+      f2_unpack(acc_pb.p[q], mine[p.C + 2 * q], mine[p.C + 2 * q + 1]);
+      f2_unpack(p1.p[q], mine[2 * p.C + 2 * q], mine[2 * p.C + 2 * q + 1]);
+      f2_unpack(p0.p[q], mine[3 * p.C + 2 * q], mine[3 * p.C + 2 * q + 1]);
     }
   }
   __syncthreads();
@@ -514,10 +816,11 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   }
 }
 
-// Adds the CTAs' partials in a fixed order and forms the parameters' gradients. Blocks x < ceil(C / 32)
-// with y == 0 own 32 channels; the rows y > 0 own the gate rows whose group several workers shared.
+// Adds the CTAs' partials in a fixed order and forms the parameters' gradients; a CTA owns 32 channels, its
+// 16 warps every 16th partial. CTAs y == 0: the column sums. CTAs y > 0: the gate rows whose group
+// several workers shared.
 template <class T>
-__global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, const NormBwdShape g,
+__global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, const NormShape g,
                                                      int ctas) {
   __shared__ float part[4][16][32];
   griddep_wait();
@@ -528,6 +831,7 @@ __global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, cons
   if (blockIdx.y == 0) {
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     if (c < p.C)
+#pragma unroll 4
       for (int b = warp; b < ctas; b += 16)
 #pragma unroll
         for (int q = 0; q < 4; ++q) s[q] += p.partial[((size_t)b * 4 + q) * p.C + c];
@@ -559,92 +863,94 @@ __global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, cons
     if (p.dpost_b) p.dpost_b[c] = scale * s[3];
     return;
   }
-  // Gate rows: one warp a group, in turn.
-  if (c >= p.C) return;
   const long long groups = (p.rows + p.rows_per_gate - 1) / p.rows_per_gate;
-  const long long step = (long long)(gridDim.y - 1) * 16;
-  for (long long gr = (long long)(blockIdx.y - 1) * 16 + warp; gr < groups; gr += step) {
+  for (long long gr = blockIdx.y - 1; gr < groups; gr += gridDim.y - 1) {
     const long long g0 = gr * p.rows_per_gate;
     long long g1 = g0 + p.rows_per_gate;
     if (g1 > p.rows) g1 = p.rows;
     const long long w0 = g0 / g.rows_per_worker, w1 = (g1 - 1) / g.rows_per_worker;
     if (w0 == w1) continue;   // one worker's: written by it
     float s = 0.f;
-    for (long long w = w0; w <= w1; ++w)
-      s += p.gate_partial[(w * 2 + (g0 > w * g.rows_per_worker ? 1 : 0)) * p.C + c];
-    p.dgate[gr * p.C + c] = s;
+    if (c < p.C)
+#pragma unroll 4
+      for (long long w = w0 + warp; w <= w1; w += 16)
+        s += p.gate_partial[(w * 2 + (g0 > w * g.rows_per_worker ? 1 : 0)) * p.C + c];
+    part[0][warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < p.C) {
+      s = 0.f;
+      for (int w = 0; w < 16; ++w) s += part[0][w][lane];
+      p.dgate[gr * p.C + c] = s;
+    }
+    __syncthreads();
   }
 }
 
-// The workers' geometry; `ctas` CTAs at most are planned for.
-static NormBwdShape bwd_shape(long long rows, int C, int es, bool pre, int* R, int* ctas) {
-  NormBwdShape g;
-  g.wpg = (C / 8 + 31) / 32;
-  g.rl = (kNormThreads / 32) / g.wpg;
-  g.tensors = pre ? 4 : 2;
-  const int row = g.tensors * C * es;
-  // Two rows at a time share the row sums' barriers; one where two would leave fewer than three
-  // stages.
-  *R = kNormRingBytes / (g.rl * 2 * row) >= 3 ? 2 : 1;
-  while (g.rl > 1 && kNormRingBytes / (g.rl * *R * row) < 2) --g.rl;
-  g.stage_bytes = *R * row;
-  g.stages = kNormRingBytes / (g.rl * g.stage_bytes);
-  if (g.stages > kNormMaxStages) g.stages = kNormMaxStages;
-  const long long most = (long long)kNormMaxCtas * g.rl;
-  g.rows_per_worker = (rows + most - 1) / most;
-  if (g.rows_per_worker < 1) g.rows_per_worker = 1;
-  g.workers = (int)((rows + g.rows_per_worker - 1) / g.rows_per_worker);
-  *ctas = (g.workers + g.rl - 1) / g.rl;
+// Two rows a step, or one where two would not leave two stages.
+static NormShape bwd_shape(long long rows, int C, int es, bool pre, int* R) {
+  *R = 2;
+  NormShape g = norm_shape(rows, C, es, pre ? 4 : 2, 2, 16);
+  if (g.stages < 2 || g.rl < (kNormThreads / 32) / g.wpg) {
+    *R = 1;
+    g = norm_shape(rows, C, es, pre ? 4 : 2, 1, 16);
+  }
   return g;
 }
+static int norm_ctas(const NormShape& g) { return (g.workers + g.rl - 1) / g.rl; }
 
 size_t norm_backward_partial(long long rows, int C, int es, bool pre, bool gate,
                              size_t* gate_offset) {
-  int R, ctas;
-  const NormBwdShape g = bwd_shape(rows, C, es, pre, &R, &ctas);
-  *gate_offset = (size_t)ctas * 4 * C * sizeof(float);
-  return *gate_offset + (gate ? (size_t)ctas * g.rl * 2 * C * sizeof(float) : 0);
+  int R;
+  const NormShape g = bwd_shape(rows, C, es, pre, &R);
+  *gate_offset = (size_t)norm_ctas(g) * 4 * C * sizeof(float);
+  return *gate_offset + (gate ? (size_t)norm_ctas(g) * g.rl * 2 * C * sizeof(float) : 0);
 }
 
-template <class T, int R>
-static cudaError_t launch_bwd(const NormBwdParams& p, const NormBwdShape& g, int ctas, int* status,
+template <class T, int R, bool PRE, bool POST>
+static cudaError_t launch_bwd(const NormBwdParams& p, const NormShape& g, int* status,
                               cudaStream_t st) {
-  size_t smem = (size_t)g.rl * g.stages * g.stage_bytes;
+  size_t smem = (size_t)g.rl * g.stages * g.stage_bytes +
+                (p.gate ? (size_t)g.rl * 2 * p.C * sizeof(float) : 0);
   const size_t sums = (size_t)g.rl * 4 * p.C * sizeof(float);
   if (sums > smem) smem = sums;
-  cudaError_t e = cudaFuncSetAttribute(k_norm_residual_backward<T, R>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       kNormRingBytes);
+  const auto kernel = k_norm_residual_backward<T, R, PRE, POST>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kNormRingBytes + 2 * kMaxNormC * (int)sizeof(float));
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_norm_residual_backward<T, R>, dim3(ctas), dim3(kNormThreads), smem, st, p, g,
-                    status);
+  return launch_pdl(kernel, dim3(norm_ctas(g)), dim3(kNormThreads), smem, st, p, g, status);
 }
 
 cudaError_t launch_norm_backward(const NormBwdParams& p, int dtype, int* status, cudaStream_t st) {
   if (p.rows == 0) return cudaSuccess;
-  const int es = dtype == SS_F32 ? 4 : 2;
-  int R, ctas;
-  const NormBwdShape g = bwd_shape(p.rows, p.C, es, p.pre_w != nullptr, &R, &ctas);
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
-    return R == 2 ? launch_bwd<T, 2>(p, g, ctas, status, st)
-                  : launch_bwd<T, 1>(p, g, ctas, status, st);
+    int R;
+    const NormShape g = bwd_shape(p.rows, p.C, sizeof(typename T::Store), p.pre_w != nullptr, &R);
+    auto go = [&](auto r) {
+      constexpr int kR = decltype(r)::value;
+      if (p.pre_w)
+        return p.post_w ? launch_bwd<T, kR, true, true>(p, g, status, st)
+                        : launch_bwd<T, kR, true, false>(p, g, status, st);
+      return p.post_w ? launch_bwd<T, kR, false, true>(p, g, status, st)
+                      : launch_bwd<T, kR, false, false>(p, g, status, st);
+    };
+    return R == 2 ? go(std::integral_constant<int, 2>{}) : go(std::integral_constant<int, 1>{});
   });
 }
 
 cudaError_t launch_norm_reduce(const NormBwdParams& p, int dtype, cudaStream_t st) {
-  const int es = dtype == SS_F32 ? 4 : 2;
-  int R, ctas;
-  const NormBwdShape g = bwd_shape(p.rows, p.C, es, p.pre_w != nullptr, &R, &ctas);
-  if (p.rows == 0) ctas = 0;   // sums over no rows: zeros
-  int ny = 1;
-  if (p.dgate && p.rows > 0) {
-    const long long groups = (p.rows + p.rows_per_gate - 1) / p.rows_per_gate;
-    ny += (int)((groups + 15) / 16 < 64 ? (groups + 15) / 16 : 64);
-  }
-  const dim3 grid((p.C + 31) / 32, ny);
   return by_dtype(dtype, [&](auto t) {
-    return launch_pdl(k_norm_reduce<decltype(t)>, grid, dim3(512), 0, st, p, g, ctas);
+    using T = decltype(t);
+    int R;
+    const NormShape g = bwd_shape(p.rows, p.C, sizeof(typename T::Store), p.pre_w != nullptr, &R);
+    const int ctas = p.rows == 0 ? 0 : norm_ctas(g);   // sums over no rows: zeros
+    long long ny = 1;
+    if (p.dgate && p.rows > 0) {
+      const long long groups = (p.rows + p.rows_per_gate - 1) / p.rows_per_gate;
+      ny += groups < 64 ? groups : 64;
+    }
+    return launch_pdl(k_norm_reduce<T>, dim3((p.C + 31) / 32, (unsigned)ny), dim3(512), 0, st, p, g,
+                      ctas);
   });
 }
 

@@ -56,6 +56,18 @@ __device__ __forceinline__ void chunk_load(Chunk<T>& c, const typename T::Store*
     c.w[4 * i + 3] = v.w;
   }
 }
+// The same from global memory that nothing writes while the kernel runs (parameters).
+template <class T>
+__device__ __forceinline__ void chunk_ldg(Chunk<T>& c, const typename T::Store* p) {
+#pragma unroll
+  for (int i = 0; i < T::kWords / 4; ++i) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    c.w[4 * i] = v.x;
+    c.w[4 * i + 1] = v.y;
+    c.w[4 * i + 2] = v.z;
+    c.w[4 * i + 3] = v.w;
+  }
+}
 template <class T>
 __device__ __forceinline__ void chunk_store(typename T::Store* p, const Chunk<T>& c) {
 #pragma unroll
