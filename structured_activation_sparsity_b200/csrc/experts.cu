@@ -4,6 +4,9 @@
 //
 // The row moves are bound by HBM: one warp a token, so that a token's own row crosses once however
 // many experts it goes to. The router and the sort are bound by latency.
+#include <algorithm>
+#include <type_traits>
+
 #include "kernels.h"
 #include "rows.cuh"
 
@@ -21,37 +24,68 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-// One warp a token, V logits a lane (expert v * 32 + lane). Each of the k rounds takes the largest key
-// left (two warp reductions: the key, then the lowest expert that has it).
+// L lanes a token (32 / L tokens a warp), V logits a lane (expert v * L + lane): with eight logits a lane a
+// round of the top-k is a few compares and log2 L shuffles for several tokens at once, where a whole
+// warp a token spends two warp reductions on each. Each round takes the largest key left and the lowest
+// expert that has it.
+template <int L>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const uint32_t w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = v > w ? v : w;
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ int group_min(int v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) {
+    const int w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = v < w ? v : w;
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
 template <int V>
-__global__ void __launch_bounds__(256) k_expert_route(const float* __restrict__ logits,
-                                                      int32_t* __restrict__ ids,
-                                                      float* __restrict__ weight, int T, int E,
-                                                      int topk, int renorm) {
+__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];
+  return best;
+}
+
+constexpr int kRouteWarps = 4;
+
+template <int V, int L>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    k_expert_route(const float* __restrict__ logits, int32_t* __restrict__ ids,
+                   float* __restrict__ weight, int T, int E, int topk, int renorm) {
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= T) return;
+  const int l = threadIdx.x % L;
+  const int t = (blockIdx.x * (kRouteWarps * 32) + threadIdx.x) / L;
+  const bool live = t < T;
   uint32_t key[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = v * 32 + lane;
-    key[v] = e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
+    const int e = v * L + l;
+    key[v] = live && e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
   }
   float top = 0.f, total = 0.f, mine = 0.f;
   int my_id = -1;
   for (int j = 0; j < topk; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];
-    best = __reduce_max_sync(0xffffffffu, best);
-    if (best == 0u) break;   // every expert left is closed
+    const uint32_t best = group_max<L>(largest(key));
     int at = 1 << 30;
 #pragma unroll
     for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) at = v * 32 + lane;
-    at = __reduce_min_sync(0xffffffffu, at);
+      if (key[v] == best) at = v * L + l;
+    at = group_min<L>(at);
     const float value = key_value(best);
     if (j == 0) {
       top = value;
@@ -60,117 +94,132 @@ __global__ void __launch_bounds__(256) k_expert_route(const float* __restrict__ 
 #pragma unroll
         for (int v = 0; v < V; ++v)
           if (key[v]) s += expf(key_value(key[v]) - top);
-        total = warp_sum(s);
+        total = group_sum<L>(s);
       }
     }
-    const float ex = expf(value - top);
+    const bool open = best != 0u;   // else every expert left is closed
+    const float ex = open ? expf(value - top) : 0.f;
     if (renorm) total += ex;
-    if (lane == j) {
+    if (l == j && open) {
       mine = ex;
       my_id = at;
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v * 32 + lane == at) key[v] = 0u;
+      if (v * L + l == at) key[v] = 0u;
   }
-  if (lane < topk) {
-    ids[(size_t)t * topk + lane] = my_id;
-    weight[(size_t)t * topk + lane] = my_id >= 0 ? mine / total : 0.f;
+  if (live && l < topk) {
+    ids[(size_t)t * topk + l] = my_id;
+    weight[(size_t)t * topk + l] = my_id >= 0 ? mine / total : 0.f;
   }
-}
-
-cudaError_t launch_expert_route(const float* logits, int32_t* ids, float* weight, int T, int E,
-                                int topk, bool renorm, cudaStream_t st) {
-  const dim3 grid((T + 7) / 8), block(256);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, st, logits, ids, weight, T, E, topk,
-                      renorm ? 1 : 0);
-  };
-  if (E <= 32) return go(k_expert_route<1>);
-  if (E <= 64) return go(k_expert_route<2>);
-  if (E <= 128) return go(k_expert_route<4>);
-  if (E <= 256) return go(k_expert_route<8>);
-  return go(k_expert_route<16>);
 }
 
 // Gradient of the weights for the logits. Renormalised: w is the softmax of the chosen logits, so
 // dlogit_j = w_j (dw_j - sum_i dw_i w_i) there and zero elsewhere. Otherwise w_j = p[id_j] of the
 // softmax p over all open experts: dlogit_e = p_e (dw_e - sum_i dw_i w_i), dw_e = 0 if not chosen.
-template <int V>
-__global__ void __launch_bounds__(256)
+template <int V, int L>
+__global__ void __launch_bounds__(kRouteWarps * 32)
     k_expert_route_backward(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                             const float* __restrict__ weight, const float* __restrict__ dweight,
                             float* __restrict__ dlogits, int T, int E, int topk, int renorm,
                             int* status) {
   griddep_wait();
   griddep_launch();
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= T) return;
+  const int l = threadIdx.x % L;
+  const int t = (blockIdx.x * (kRouteWarps * 32) + threadIdx.x) / L;
+  const bool live = t < T;
   int id = -1;
   float w = 0.f, dw = 0.f;
-  if (lane < topk) {
-    id = __ldg(ids + (size_t)t * topk + lane);
+  if (live && l < topk) {
+    id = __ldg(ids + (size_t)t * topk + l);
     if (id < -1 || id >= E) {
       record_bad_index(status);
       id = -1;
     }
     if (id >= 0) {
-      w = __ldg(weight + (size_t)t * topk + lane);
-      dw = __ldg(dweight + (size_t)t * topk + lane);
+      w = __ldg(weight + (size_t)t * topk + l);
+      dw = __ldg(dweight + (size_t)t * topk + l);
     }
   }
-  const float mean = warp_sum(w * dw);
   float d[V];
-  if (renorm) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = 0.f;
-  } else {
-    uint32_t key[V], best = 0u;
+  for (int v = 0; v < V; ++v) d[v] = 0.f;
+  const float mean = group_sum<L>(w * dw);
+  if (!renorm) {
+    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int e = v * 32 + lane;
-      key[v] = e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
-      best = best > key[v] ? best : key[v];
+      const int e = v * L + l;
+      key[v] = live && e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
     }
-    best = __reduce_max_sync(0xffffffffu, best);
-    const float top = best ? key_value(best) : 0.f;
+    const uint32_t best = group_max<L>(largest(key));
+    const float top = key_value(best);
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      d[v] = key[v] ? expf(key_value(key[v]) - top) : 0.f;
+      if (key[v]) d[v] = expf(key_value(key[v]) - top);
       s += d[v];
     }
-    const float total = warp_sum(s);
+    const float total = group_sum<L>(s);
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = d[v] > 0.f ? -mean * (d[v] / total) : 0.f;
+    for (int v = 0; v < V; ++v) d[v] = key[v] ? -mean * (d[v] / total) : 0.f;
   }
+  const float add = renorm ? w * (dw - mean) : w * dw;
   for (int j = 0; j < topk; ++j) {
-    const int e = __shfl_sync(0xffffffffu, id, j);
-    const float add = __shfl_sync(0xffffffffu, renorm ? w * (dw - mean) : w * dw, j);
+    const int e = __shfl_sync(0xffffffffu, id, j, L);
+    const float a = __shfl_sync(0xffffffffu, add, j, L);
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v * 32 + lane == e) d[v] += add;
+      if (v * L + l == e) d[v] += a;
   }
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    if (v * 32 + lane < E) dlogits[(size_t)t * E + v * 32 + lane] = d[v];
+    if (live && v * L + l < E) dlogits[(size_t)t * E + v * L + l] = d[v];
+}
+
+// The lanes a token takes: at least topk (each writes one expert), and no more than eight logits a lane
+// until a warp is full.
+template <class F>
+static cudaError_t by_experts(int E, int topk, F&& go) {
+  using std::integral_constant;
+  int L = 4;
+  while (L < 32 && (L < topk || L * 8 < E)) L *= 2;
+  const int v = (E + L - 1) / L;
+  auto with = [&](auto l) {
+    if (v <= 1) return go(integral_constant<int, 1>{}, l);
+    if (v <= 2) return go(integral_constant<int, 2>{}, l);
+    if (v <= 4) return go(integral_constant<int, 4>{}, l);
+    if (v <= 8) return go(integral_constant<int, 8>{}, l);
+    return go(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+  };
+  if (L == 4) return with(integral_constant<int, 4>{});
+  if (L == 8) return with(integral_constant<int, 8>{});
+  if (L == 16) return with(integral_constant<int, 16>{});
+  return with(integral_constant<int, 32>{});
+}
+static dim3 route_grid(int T, int L) {
+  const int per = kRouteWarps * 32 / L;
+  return dim3((T + per - 1) / per);
+}
+
+cudaError_t launch_expert_route(const float* logits, int32_t* ids, float* weight, int T, int E,
+                                int topk, bool renorm, cudaStream_t st) {
+  return by_experts(E, topk, [&](auto v, auto l) {
+    return launch_pdl(k_expert_route<decltype(v)::value, decltype(l)::value>,
+                      route_grid(T, decltype(l)::value), dim3(kRouteWarps * 32), 0, st, logits, ids,
+                      weight, T, E, topk, renorm ? 1 : 0);
+  });
 }
 
 cudaError_t launch_expert_route_backward(const float* logits, const int32_t* ids,
                                          const float* weight, const float* dweight, float* dlogits,
                                          int T, int E, int topk, bool renorm, int* status,
                                          cudaStream_t st) {
-  const dim3 grid((T + 7) / 8), block(256);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, st, logits, ids, weight, dweight, dlogits, T, E,
-                      topk, renorm ? 1 : 0, status);
-  };
-  if (E <= 32) return go(k_expert_route_backward<1>);
-  if (E <= 64) return go(k_expert_route_backward<2>);
-  if (E <= 128) return go(k_expert_route_backward<4>);
-  if (E <= 256) return go(k_expert_route_backward<8>);
-  return go(k_expert_route_backward<16>);
+  return by_experts(E, topk, [&](auto v, auto l) {
+    return launch_pdl(k_expert_route_backward<decltype(v)::value, decltype(l)::value>,
+                      route_grid(T, decltype(l)::value), dim3(kRouteWarps * 32), 0, st, logits, ids,
+                      weight, dweight, dlogits, T, E, topk, renorm ? 1 : 0, status);
+  });
 }
 
 // ---- sort -----------------------------------------------------------------------------------
@@ -229,6 +278,7 @@ __global__ void __launch_bounds__(kSortThreads)
                    int32_t* __restrict__ order, int32_t* __restrict__ slot,
                    int32_t* __restrict__ offsets, int n, int chunk, int E, int* status) {
   extern __shared__ int counts[];   // [warps][E]: counts, then the next place of each expert
+  __shared__ int2 s_part[kSortThreads];
   __shared__ int s_sum[kSortWarps];
   __shared__ int s_total;
   griddep_wait();
@@ -241,20 +291,32 @@ __global__ void __launch_bounds__(kSortThreads)
   const int a0 = min(c1, c0 + warp * part), a1 = min(c1, c0 + (warp + 1) * part);
   sort_count(ids, a0, a1, E, counts + warp * E, status);
   __syncthreads();
-  // Thread e (E <= the CTA's threads): its expert's total over all CTAs and over those before.
+  // Thread e (E <= the CTA's threads): its expert's total over all CTAs and over those before. The CTAs'
+  // counts are read by all threads, `parts` of them an expert, so that few loads follow one another.
   int total = 0, before = 0;
   const int e = threadIdx.x;
-  if (e < E) {
-    if (gridDim.x == 1) {
+  if (gridDim.x == 1) {
+    if (e < E)
       for (int w = 0; w < kSortWarps; ++w) total += counts[w * E + e];
-    } else {
-#pragma unroll 8
-      for (int b = 0; b < gridDim.x; ++b) {
-        const int h = __ldg(hist + (size_t)b * E + e);
-        total += h;
-        before += b < blockIdx.x ? h : 0;
+  } else {
+    const int parts = kSortThreads / E, part_of = threadIdx.x / E, ex = threadIdx.x % E;
+    int sum = 0, sum_before = 0;
+    if (part_of < parts) {
+#pragma unroll 16
+      for (int b = part_of; b < gridDim.x; b += parts) {
+        const int h = __ldg(hist + (size_t)b * E + ex);
+        sum += h;
+        sum_before += b < blockIdx.x ? h : 0;
       }
     }
+    s_part[threadIdx.x] = make_int2(sum, sum_before);
+    __syncthreads();
+    if (e < E)
+      for (int q = 0; q < parts; ++q) {
+        const int2 v = s_part[q * E + e];
+        total += v.x;
+        before += v.y;
+      }
   }
   // Exclusive sum of the totals over the experts.
   int x = total;
@@ -390,18 +452,121 @@ cudaError_t launch_expert_gather(const void* x, const int32_t* slot, void* xs, i
 }
 
 // out[t] = residual[t] + sum_j weight[t, j] * ys[slot[t, j]], the sum in fp32 in the order of j, then the
-// residual. Y: the sorted rows' type (fp32 partials of `splits` k-splits, `split_stride` apart, are
-// added first, in split order).
-template <class T, class Y>
-__global__ void __launch_bounds__(256)
-    k_expert_combine(const typename Y::Store* __restrict__ ys, const int32_t* __restrict__ slot,
+// residual. A warp takes 32 U chunks of a token (`parts` warps a token) with all of its rows' loads in
+// flight together, and has the next token's slots and weights on their way meanwhile, so that each
+// token waits for memory once. K: topk where it is at most kCombineK (every row's raw words are held until
+// they are added, chunk by chunk), else 0 (four experts at a time into running sums).
+constexpr int kCombineK = 4;
+constexpr int kCombineCtas = 3;   // CTAs an SM
+
+template <class T, int U, int K>
+__global__ void __launch_bounds__(256, kCombineCtas)
+    k_expert_combine(const typename T::Store* __restrict__ ys, const int32_t* __restrict__ slot,
                      const float* __restrict__ weight, const typename T::Store* residual,
-                     typename T::Store* out, int tokens, int topk, int C, long long ld, int splits,
-                     long long split_stride, int* status) {
+                     typename T::Store* out, int tokens, int topk, int C, long long ld, int parts,
+                     int* status) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long items = (long long)tokens * parts, step = (long long)gridDim.x * 8;
+  const int chunks = C / 8;
+  if (K > 0) topk = K;
+  auto lookup = [&](long long item, int& p, float& w) {
+    p = -1;
+    w = 0.f;
+    if (item < items && lane < topk) {
+      const long long a = item / parts * topk + lane;
+      p = row_slot(slot, a, tokens * topk, status);
+      w = weight ? __ldg(weight + a) : 1.f;
+    }
+  };
+  long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  int my;
+  float my_w;
+  lookup(item, my, my_w);
+  for (; item < items; item += step) {
+    const long long t = item / parts;
+    const int c0 = (int)(item - t * parts) * 32 * U + lane;
+    int next;
+    float next_w;
+    Chunk<T> res[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      chunk_zero(res[i]);
+      if (residual && c0 + 32 * i < chunks)
+        chunk_load(res[i], residual + t * ld + (c0 + 32 * i) * 8);
+    }
+    constexpr int kJ = K > 0 ? K : 4;   // experts whose rows are in flight together
+    Chunk<T> y[kJ][U];
+    int p[kJ];
+    auto load = [&](int j0) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        p[j] = __shfl_sync(0xffffffffu, my, (j0 + j) & 31);
+        if (j0 + j >= topk) p[j] = -1;
+        if (p[j] < 0) continue;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (c0 + 32 * i < chunks) chunk_load(y[j][i], ys + (size_t)p[j] * C + (c0 + 32 * i) * 8);
+      }
+    };
+    auto add = [&](int j0, int i, float (&acc)[8]) {
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const float w = __shfl_sync(0xffffffffu, my_w, (j0 + j) & 31);
+        if (p[j] < 0) continue;
+        float f[8];
+        chunk_floats(y[j][i], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) acc[q] += w * f[q];
+      }
+    };
+    auto finish = [&](int i, float (&acc)[8]) {
+      if (c0 + 32 * i >= chunks) return;
+      float r[8];
+      chunk_floats(res[i], r);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) acc[q] += r[q];
+      Chunk<T> o;
+      chunk_round(o, acc);
+      chunk_store(out + t * ld + (c0 + 32 * i) * 8, o);
+    };
+    if constexpr (K > 0) {
+      load(0);
+      lookup(item + step, next, next_w);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        float acc[8] = {};
+        add(0, i, acc);
+        finish(i, acc);
+      }
+    } else {
+      float acc[U][8] = {};
+      for (int j0 = 0; j0 < topk; j0 += kJ) {
+        load(j0);
+        if (j0 == 0) lookup(item + step, next, next_w);
+#pragma unroll
+        for (int i = 0; i < U; ++i) add(j0, i, acc[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) finish(i, acc[i]);
+    }
+    my = next;
+    my_w = next_w;
+  }
+}
+
+// The same over fp32 partials [splits][tokens * topk][C] of fc2's k-splits, added in split order; one chunk a lane.
+__global__ void __launch_bounds__(256)
+    k_expert_combine_splits(const float* __restrict__ ys, const int32_t* __restrict__ slot,
+                            const float* __restrict__ weight, const uint16_t* residual,
+                            uint16_t* out, int tokens, int topk, int C, long long ld, int parts,
+                            int splits, int* status) {
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int t = (int)(item / parts), c = ((int)(item % parts) * 32 + lane) * 8;
   if (t >= tokens) return;
   int my = -1;
   float my_w = 0.f;
@@ -409,86 +574,105 @@ __global__ void __launch_bounds__(256)
     my = row_slot(slot, (long long)t * topk + lane, tokens * topk, status);
     my_w = weight ? __ldg(weight + (size_t)t * topk + lane) : 1.f;
   }
-  const int chunks = C / 8;
-  for (int cb = 0; cb < chunks; cb += 64) {
-    float acc[2][8];
-    Chunk<T> res[2];
+  float acc[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      chunk_zero(res[i]);
+  for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+  const long long step = (long long)tokens * topk * C;
+  for (int j = 0; j < topk; ++j) {
+    const int p = __shfl_sync(0xffffffffu, my, j);
+    const float w = __shfl_sync(0xffffffffu, my_w, j);
+    if (p < 0 || c >= C) continue;
+    float f[8];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc[i][q] = 0.f;
-      const int c = cb + 32 * i + lane;
-      if (residual && c < chunks) chunk_load(res[i], residual + (size_t)t * ld + c * 8);
-    }
+    for (int q = 0; q < 8; ++q) f[q] = 0.f;
 #pragma unroll 4
-    for (int j = 0; j < topk; ++j) {
-      const int p = __shfl_sync(0xffffffffu, my, j);
-      const float w = __shfl_sync(0xffffffffu, my_w, j);
-      if (p < 0) continue;
+    for (int s = 0; s < splits; ++s) {
+      Chunk<F32> v;
+      float g[8];
+      chunk_load(v, ys + s * step + (size_t)p * C + c);
+      chunk_floats(v, g);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = cb + 32 * i + lane;
-        if (c >= chunks) continue;
-        float f[8];
-        Chunk<Y> v;
-        chunk_load(v, ys + (size_t)p * C + c * 8);
-        chunk_floats(v, f);
-        for (int s = 1; s < splits; ++s) {
-          float g[8];
-          chunk_load(v, ys + s * split_stride + (size_t)p * C + c * 8);
-          chunk_floats(v, g);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) f[q] += g[q];
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) acc[i][q] += w * f[q];
-      }
+      for (int q = 0; q < 8; ++q) f[q] += g[q];
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int c = cb + 32 * i + lane;
-      if (c >= chunks) continue;
-      float r[8];
-      chunk_floats(res[i], r);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) acc[i][q] += r[q];
-      Chunk<T> o;
-      chunk_round(o, acc[i]);
-      chunk_store(out + (size_t)t * ld + c * 8, o);
-    }
+    for (int q = 0; q < 8; ++q) acc[q] += w * f[q];
   }
+  if (c >= C) return;
+  Chunk<Bf16> o;
+  if (residual) {
+    float r[8];
+    chunk_load(o, residual + (size_t)t * ld + c);
+    chunk_floats(o, r);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] += r[q];
+  }
+  chunk_round(o, acc);
+  chunk_store(out + (size_t)t * ld + c, o);
 }
 
 cudaError_t launch_expert_combine(const void* ys, const int32_t* slot, const float* weight,
                                   const void* residual, void* out, int tokens, int topk, int C,
                                   long long ld, int dtype, int splits, int* status,
                                   cudaStream_t st) {
+  const int chunks = C / 8;
+  auto grid = [&](int parts) {
+    return dim3((unsigned)(((long long)tokens * parts + 7) / 8));
+  };
+  if (splits > 0) {
+    const int parts = (chunks + 31) / 32;
+    return launch_pdl(k_expert_combine_splits, grid(parts), dim3(256), 0, st,
+                      static_cast<const float*>(ys), slot, weight,
+                      static_cast<const uint16_t*>(residual), static_cast<uint16_t*>(out), tokens,
+                      topk, C, ld, parts, splits, status);
+  }
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     using S = typename T::Store;
-    auto go = [&](auto y) {
-      using Y = decltype(y);
-      return launch_pdl(k_expert_combine<T, Y>, dim3((tokens + 7) / 8), dim3(256), 0, st,
-                        static_cast<const typename Y::Store*>(ys), slot, weight,
-                        static_cast<const S*>(residual), static_cast<S*>(out), tokens, topk, C, ld,
-                        splits > 1 ? splits : 1, (long long)tokens * topk * C, status);
+    auto go = [&](auto u, auto k) {
+      constexpr int U = decltype(u)::value, K = decltype(k)::value;
+      const int parts = (chunks + 32 * U - 1) / (32 * U);
+      const int ctas = (int)std::min<long long>(((long long)tokens * parts + 7) / 8,
+                                                kCombineCtas * kRowCtas);
+      return launch_pdl(k_expert_combine<T, U, K>, dim3(ctas), dim3(256), 0, st,
+                        static_cast<const S*>(ys), slot, weight, static_cast<const S*>(residual),
+                        static_cast<S*>(out), tokens, topk, C, ld, parts, status);
     };
-    return splits > 0 ? go(F32{}) : go(t);
+    using std::integral_constant;
+    // As few warps a token as hold its rows' words in registers, its chunks spread evenly; one chunk a
+    // lane where there are few tokens.
+    auto with = [&](auto k, auto most) {
+      constexpr int kMost = decltype(most)::value;
+      const int lanes = (chunks + 31) / 32, parts = (lanes + kMost - 1) / kMost;
+      const bool few = (long long)tokens * lanes <= 8 * kCombineCtas * kRowCtas;
+      const int u = few ? 1 : (lanes + parts - 1) / parts;
+      if (u == 1) return go(integral_constant<int, 1>{}, k);
+      if (u == 2) return go(integral_constant<int, kMost < 2 ? 1 : 2>{}, k);
+      if (u == 3) return go(integral_constant<int, kMost < 3 ? 1 : 3>{}, k);
+      if (u == 4) return go(integral_constant<int, kMost < 4 ? 1 : 4>{}, k);
+      return go(integral_constant<int, kMost < 5 ? 1 : 5>{}, k);
+    };
+    constexpr bool kWide = T::kWords == 8;
+    switch (topk) {
+      case 1: return with(integral_constant<int, 1>{}, integral_constant<int, kWide ? 3 : 5>{});
+      case 2: return with(integral_constant<int, 2>{}, integral_constant<int, kWide ? 2 : 4>{});
+      case 3: return with(integral_constant<int, 3>{}, integral_constant<int, kWide ? 1 : 3>{});
+      case 4: return with(integral_constant<int, 4>{}, integral_constant<int, kWide ? 1 : 2>{});
+      default: return with(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+    }
   });
 }
 
 // The combine's gradient: dys[slot[t, j]] = weight[t, j] * dout[t] (rounded once) and
-// dweight[t, j] = dout[t] . ys[slot[t, j]], in one walk over the token's chunks (K assignments' dot
-// products at a time).
-template <class T>
+// dweight[t, j] = dout[t] . ys[slot[t, j]]. One warp a token, which the dot products need; two experts and
+// U chunks a lane at a time, all their loads in flight together.
+template <class T, int U>
 __global__ void __launch_bounds__(256)
     k_expert_combine_backward(const typename T::Store* __restrict__ dout,
                               const typename T::Store* ys, const int32_t* __restrict__ slot,
                               const float* __restrict__ weight, typename T::Store* dys,
                               float* __restrict__ dweight, int tokens, int topk, int C,
                               long long ld, int* status) {
-  constexpr int K = 4;
+  constexpr int K = 2;
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -512,26 +696,35 @@ __global__ void __launch_bounds__(256)
       if (j0 + q >= topk) p[q] = -1;
       dot[q] = 0.f;
     }
-    for (int c = lane; c < chunks; c += 32) {
-      Chunk<T> d, y[K];
-      chunk_load(d, dout + (size_t)t * ld + c * 8);
+    for (int c0 = lane; c0 < chunks; c0 += 32 * U) {
+      Chunk<T> d[U], y[K][U];
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (c0 + 32 * i < chunks) chunk_load(d[i], dout + (size_t)t * ld + (c0 + 32 * i) * 8);
 #pragma unroll
       for (int q = 0; q < K; ++q)
-        if (p[q] >= 0) chunk_load(y[q], ys + (size_t)p[q] * C + c * 8);
-      float df[8];
-      chunk_floats(d, df);
 #pragma unroll
-      for (int q = 0; q < K; ++q) {
-        if (p[q] < 0) continue;
-        float yf[8];
-        chunk_floats(y[q], yf);
+        for (int i = 0; i < U; ++i)
+          if (p[q] >= 0 && c0 + 32 * i < chunks)
+            chunk_load(y[q][i], ys + (size_t)p[q] * C + (c0 + 32 * i) * 8);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dot[q] += df[i] * yf[i];
+      for (int i = 0; i < U; ++i) {
+        if (c0 + 32 * i >= chunks) continue;
+        float df[8];
+        chunk_floats(d[i], df);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) yf[i] = w[q] * df[i];
-        Chunk<T> o;
-        chunk_round(o, yf);
-        chunk_store(dys + (size_t)p[q] * C + c * 8, o);
+        for (int q = 0; q < K; ++q) {
+          if (p[q] < 0) continue;
+          float yf[8];
+          chunk_floats(y[q][i], yf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) dot[q] += df[e] * yf[e];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) yf[e] = w[q] * df[e];
+          Chunk<T> o;
+          chunk_round(o, yf);
+          chunk_store(dys + (size_t)p[q] * C + (c0 + 32 * i) * 8, o);
+        }
       }
     }
 #pragma unroll
@@ -550,7 +743,8 @@ cudaError_t launch_expert_combine_backward(const void* dout, const void* ys, con
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     using S = typename T::Store;
-    return launch_pdl(k_expert_combine_backward<T>, dim3((tokens + 7) / 8), dim3(256), 0, st,
+    constexpr int U = T::kWords == 8 ? 2 : 4;
+    return launch_pdl(k_expert_combine_backward<T, U>, dim3((tokens + 7) / 8), dim3(256), 0, st,
                       static_cast<const S*>(dout), static_cast<const S*>(ys), slot, weight,
                       static_cast<S*>(dys), dweight, tokens, topk, C, ld, status);
   });
