@@ -16,8 +16,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsparsesam.so")
 SOURCES = ["score_perm.cu", "attn.cu", "mlp.cu", "block.cu", "partial.cu", "relpos.cu", "api.cu", "noalloc.cu",
-           "norm.cu", "experts.cu", "expert_mlp.cu", "api_experts.cu"]
-HEADERS = ["common.cuh", "rows.cuh", "host.h", "kernels.h", "pattern.h"]
+           "norm.cu", "experts.cu", "api_experts.cu"]
+HEADERS = ["common.cuh", "rows.cuh", "expert_mlp.cuh", "host.h", "kernels.h", "pattern.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

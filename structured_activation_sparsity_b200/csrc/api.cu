@@ -1126,8 +1126,7 @@ uint64_t sparsesam_launch_count(void) { return g_launches.load(); }
 int sparsesam_set_wait_limit_ns(uint64_t ns) {
   const uint64_t v = ns ? ns : kWaitLimitNs;
   if (set_wait_limit_here(v) != cudaSuccess || set_wait_limit_attn(v) != cudaSuccess ||
-      set_wait_limit_mlp(v) != cudaSuccess || set_wait_limit_norm(v) != cudaSuccess ||
-      set_wait_limit_expert_mlp(v) != cudaSuccess)
+      set_wait_limit_mlp(v) != cudaSuccess || set_wait_limit_norm(v) != cudaSuccess)
     return SS_ECUDA;
   return SS_OK;
 }

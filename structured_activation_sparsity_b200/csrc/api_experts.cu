@@ -352,6 +352,17 @@ int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int3
   uint16_t* h = reinterpret_cast<uint16_t*>(wsb + L.h);
   void* y = wsb + L.y;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (expert_vec_fits(n, C, H)) {
+    rc = cuda_err(traced("expert_vec_fc1", st, [&] {
+      return launch_expert_vec_fc1(x, or_C(cfg->ld, C), ids, w1, b1, h, n, cfg->topk, E, C, H,
+                                   status, st);
+    }));
+    if (rc) return rc;
+    return cuda_err(traced("expert_vec_fc2", st, [&] {
+      return launch_expert_vec_fc2(h, ids, weight, residual, w2, b2, out, or_C(cfg->ld, C),
+                                   cfg->tokens, cfg->topk, E, C, H, status, st);
+    }));
+  }
   CUtensorMap tw1, tx, tw2, th;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_bf16(&tw1, 2, w1, C, (uint64_t)E * H, 1, (uint64_t)C * 2, 64, 128, sw) ||

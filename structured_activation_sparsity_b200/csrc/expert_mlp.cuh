@@ -1,0 +1,525 @@
+// The experts' products on tcgen05 / TMEM: for rows sorted by expert, H = GELU(X W1_e^T + b1_e) and
+// Y = H W2_e^T + b2_e, each expert over its own rows, in one launch per product.
+//
+// The product is taken transposed, D[features, rows] = W_e[features, Kd] X[rows, Kd]^T: the weights are
+// the 128-row operand and the tokens the narrow one. An expert's row count is whatever the router
+// gave it; the tensor core's N (a multiple of 16 up to 256) follows it, where an M of 128 tokens
+// would be mostly padding at a few rows an expert, and the weights, which bound that case, are always
+// read in whole tiles. With many rows a tile is 128 x 256 like the dense GEMM's.
+//
+// The row counts are on the device only (the sort's offsets): every CTA turns them into the same
+// list of tiles, and takes units (tile, feature tile, k-split) c, c + grid, c + 2 grid, ...
+//
+// Part of mlp.cu, whose GELU it uses.
+#pragma once
+
+#include "kernels.h"
+#include "rows.cuh"
+
+namespace ss {
+
+// warp 0 TMA producer, warp 1 TMEM allocation and MMA issue, warps 2-3 idle, warps 4-11 epilogue.
+constexpr int kXThreads = 384;
+constexpr int kXEpiThreads = 256;
+constexpr uint32_t kXRegsProducer = 56, kXRegsEpilogue = 224;
+static_assert(128 * kXRegsProducer + 256 * kXRegsEpilogue <= 384 * 168,
+              "expert GEMM register split too large");
+
+// Each epilogue warp turns 32 rows at a time from feature-major (a thread holds one feature) to row-major
+// in 2 KB of shared memory: 64 bytes a row, so that it stores 16 bytes a lane, eight rows an instruction.
+constexpr int kXTurn = 32 * 64;
+
+// Token tile TN: a stage holds one 64-wide k-block of 128 weight rows and TN token rows.
+template <int TN>
+struct XCfg {
+  static constexpr int kABytes = 128 * 128;
+  static constexpr int kBBytes = TN * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
+  static constexpr int kBar = kStages * kStageBytes;
+  static constexpr int kTiles = kBar + 256;                       // tile_start[E + 1], offsets[E + 1]
+  static constexpr int kTurn = kTiles + (2 * (kMaxExperts + 1) * 4 + 15) / 16 * 16;
+  static constexpr int kAlloc = kTurn + 8 * kXTurn + 1024;
+  static constexpr int kTmemCols = 2 * TN <= 32 ? 32 : 2 * TN;    // two accumulators
+  static_assert((2 * kStages + 5) * 8 <= 256, "barriers");
+};
+
+struct XUnit {
+  int e, row0, rows;     // expert, first sorted row, rows of the tile (1..TN)
+  int m0, s, kb0, kb1;   // first feature, k-split and its k-blocks
+};
+
+template <int TN>
+__global__ void __launch_bounds__(kXThreads, 1)
+    k_expert_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                  const ExpertGemm g, int* status) {
+  using G = XCfg<TN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + G::kBar);
+  uint64_t* empty = full + G::kStages;
+  uint64_t* acc_full = empty + G::kStages;   // [2]
+  uint64_t* acc_empty = acc_full + 2;        // [2]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* tile_start = reinterpret_cast<int*>(smem + G::kTiles);   // [E + 1]
+  int* offs = tile_start + kMaxExperts + 1;                     // [E + 1]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full + b, 1);
+      mbar_init(acc_empty + b, kXEpiThreads);
+    }
+    *abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, G::kTmemCols);
+  griddep_wait();
+  griddep_launch();
+  // The experts' tiles: warp 2 sums ceil(rows / TN) over the experts, 32 at a time.
+  if (warp == 2) {
+    int base = 0;
+    for (int e0 = 0; e0 < g.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int lo = e < g.E ? __ldg(g.offsets + e) : 0, hi = e < g.E ? __ldg(g.offsets + e + 1) : 0;
+      int x = (hi - lo + TN - 1) / TN;
+      const int own = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (e < g.E) {
+        tile_start[e] = base + x - own;
+        offs[e] = lo;
+        if (e == g.E - 1) {
+          tile_start[g.E] = base + x;
+          offs[g.E] = hi;
+        }
+      }
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  tc_fence_before();
+  cta_sync_converged();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int units = tile_start[g.E] * g.m_tiles * g.splits;
+
+  auto decode = [&](int u) {
+    XUnit r;
+    r.s = u % g.splits;
+    const int v = u / g.splits;
+    r.m0 = v % g.m_tiles * 128;
+    const int t = v / g.m_tiles;
+    int lo = 0, hi = g.E;   // tile_start[lo] <= t < tile_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile_start[mid] <= t) lo = mid;
+      else hi = mid;
+    }
+    r.e = lo;
+    r.row0 = offs[lo] + (t - tile_start[lo]) * TN;
+    const int left = offs[lo + 1] - r.row0;
+    r.rows = left < TN ? left : TN;
+    r.kb0 = (int)((long long)r.s * g.kb_total / g.splits);
+    r.kb1 = (int)((long long)(r.s + 1) * g.kb_total / g.splits);
+    return r;
+  };
+
+  if (warp < 4) {
+    setmaxnreg_dec<kXRegsProducer>();
+    if (warp == 0 && lane == 0) {
+      tma_prefetch_desc(&ta);
+      tma_prefetch_desc(&tb);
+      int it = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+        const XUnit r = decode(u);
+        const int nk = r.kb1 - r.kb0;
+        for (int j = 0; j < nk; ++j, ++it) {
+          const int st = it % G::kStages;
+          if (it >= G::kStages &&
+              !(ok = mbar_wait(empty + st, ((it / G::kStages) - 1) & 1, abort, status)))
+            break;
+          uint8_t* sa = smem + st * G::kStageBytes;
+          mbar_expect_tx(full + st, G::kStageBytes);
+          tma_load_2d(sa, &ta, full + st, (r.kb0 + j) * 64, r.e * g.features + r.m0);
+          tma_load_2d(sa + G::kABytes, &tb, full + st, (r.kb0 + j) * 64, r.row0);
+        }
+      }
+    } else if (warp == 1 && lane == 0) {
+      int it = 0, i = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++i) {
+        const XUnit r = decode(u);
+        const uint32_t idesc = idesc_bf16_f32(128, (r.rows + 15) & ~15, false, false);
+        const int buf = i & 1;
+        if (i >= 2 && !(ok = mbar_wait(acc_empty + buf, ((i >> 1) - 1) & 1, abort, status))) break;
+        tc_fence_after();
+        const uint32_t d = tmem + buf * TN;
+        const int nk = r.kb1 - r.kb0;
+        bool ready = mbar_test(full + it % G::kStages, (it / G::kStages) & 1);
+        for (int j = 0; j < nk; ++j, ++it) {
+          const int st = it % G::kStages;
+          if (!__builtin_expect(ready, 1) &&
+              !(ok = mbar_wait(full + st, (it / G::kStages) & 1, abort, status)))
+            break;
+          if (j + 1 < nk) ready = mbar_test(full + (it + 1) % G::kStages, ((it + 1) / G::kStages) & 1);
+          tc_fence_after();
+          const uint32_t a_addr = smem_u32(smem + st * G::kStageBytes);
+          const uint32_t b_addr = a_addr + G::kABytes;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_bf16_ss(d, smem_desc(a_addr + kk * 32, 16, 1024, kSwizzle128B),
+                         smem_desc(b_addr + kk * 32, 16, 1024, kSwizzle128B), idesc,
+                         (j > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(empty + st);
+        }
+        if (ok) umma_commit(acc_full + buf);
+      }
+    }
+  } else {
+    setmaxnreg_inc<kXRegsEpilogue>();
+    // Warp w reads TMEM lanes 32 (w % 4) ..: a thread holds one feature, and 32 rows at a time (the two
+    // warps of a lane quadrant take every other group of 32).
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t lane_off = uint32_t(32 * quad) << 16;
+    uint16_t* turn = reinterpret_cast<uint16_t*>(smem + G::kTurn + (warp - 4) * kXTurn);
+    int i = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+      const XUnit r = decode(u);
+      const int buf = i & 1;
+      const int f0 = r.m0 + 32 * quad, f = f0 + lane;
+      const bool live = f < g.features;
+      float bias = 0.f;
+      if (live && g.bias && r.s == 0)
+        bias = __uint_as_float((uint32_t)__ldg(g.bias + (size_t)r.e * g.features + f) << 16);
+      const bool ok = __all_sync(0xffffffffu, mbar_wait(acc_full + buf, (i >> 1) & 1, abort, status));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t_acc = tmem + buf * TN + lane_off;
+      for (int c = half * 32; c < r.rows; c += 64) {
+        uint32_t v[32];
+        tmem_ld32(t_acc + c, v);
+        const int n = r.rows - c < 32 ? r.rows - c : 32;
+        if (g.partial) {
+          float* out = g.partial + ((size_t)r.s * g.n + r.row0 + c) * g.features + f;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (live && e < n) out[(size_t)e * g.features] = __uint_as_float(v[e]) + bias;
+          continue;
+        }
+        __syncwarp();   // the previous group's rows have been read
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          float z0, z1;
+          f2_unpack(f2_add(f2_pack(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])),
+                           f2_pack(bias, bias)), z0, z1);
+          if (g.gelu) gelu_erf2(z0, z1);
+          const uint32_t h = pack_bf16(z0, z1);
+          turn[(2 * e) * 32 + lane] = (uint16_t)h;
+          turn[(2 * e + 1) * 32 + lane] = (uint16_t)(h >> 16);
+        }
+        __syncwarp();
+        // Eight rows an instruction, four lanes a row of 64 bytes (features are a multiple of 8).
+        const int q = lane & 3;
+        uint16_t* out = g.out + (size_t)(r.row0 + c + (lane >> 2)) * g.features + f0 + 8 * q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint4 w = reinterpret_cast<const uint4*>(turn)[e * 32 + lane];
+          if (8 * e + (lane >> 2) < n && f0 + 8 * q < g.features)
+            *reinterpret_cast<uint4*>(out + (size_t)(8 * e) * g.features) = w;
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(acc_empty + buf);
+    }
+  }
+  tc_fence_before();
+  cta_sync_converged();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::kTmemCols);
+  }
+}
+
+ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms) {
+  ExpertGemmPlan p;
+  p.m_tiles = (features + 127) / 128;
+  // The narrowest token tile that holds an average expert's rows.
+  const long long avg = (n + E - 1) / E;
+  p.tn = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
+  // Tiles at most: one per expert with rows, and one more per full tile.
+  long long tiles = n / p.tn + (n < E ? n : E);
+  if (tiles > n) tiles = n;
+  p.max_units = tiles * p.m_tiles;
+  p.splits = 1;
+  const int kb = (Kd + 63) / 64;
+  if (split)
+    while (p.splits < 8 && p.max_units * (p.splits + 1) <= sms && kb / (p.splits + 1) >= 4)
+      ++p.splits;
+  p.max_units *= p.splits;
+  return p;
+}
+
+template <int TN>
+static cudaError_t launch_x(const CUtensorMap* ta, const CUtensorMap* tb, const ExpertGemm& g,
+                            int grid, int* status, cudaStream_t st) {
+  using G = XCfg<TN>;
+  cudaError_t e = cudaFuncSetAttribute(k_expert_gemm<TN>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, G::kAlloc);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_expert_gemm<TN>, dim3(grid), dim3(kXThreads), G::kAlloc, st, *ta, *tb, g,
+                    status);
+}
+
+cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
+                               const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
+                               cudaStream_t st) {
+  const int grid = (int)(p.max_units < sms ? p.max_units : sms);
+  switch (p.tn) {
+    case 32: return launch_x<32>(ta, tb, g, grid, status, st);
+    case 64: return launch_x<64>(ta, tb, g, grid, status, st);
+    case 128: return launch_x<128>(ta, tb, g, grid, status, st);
+    default: return launch_x<256>(ta, tb, g, grid, status, st);
+  }
+}
+
+// ---- few rows -----------------------------------------------------------------------------------
+// A handful of assignments (single tokens) read an expert's weights for one row each, and that is all that
+// counts: 2 C hidden bf16 an assignment. Two launches without sort or gather: fc1 over (features,
+// assignments), fc2 over (channels, tokens), which also weights and adds the token's experts and its
+// residual. A block's eight warps are `kw` pieces of the product's K times 8 / kw groups of four weight rows;
+// a warp has its piece of all four rows (4 V 16-byte loads a lane) in flight at once. fc2 requests its first
+// weights before it waits for fc1.
+constexpr int kVecRows = 4;                    // weight rows of a warp
+constexpr int kVecMostK = 8 * 32 * 4 * 8;      // longest K: eight warps of four chunks a lane
+
+struct ExpertVec {
+  const uint16_t* x;        // fc1: [tokens, ld]; fc2: hidden rows [n, K]
+  const int32_t* ids;       // [n]
+  const uint16_t *w, *bias; // [E, rows, K], [E, rows]
+  uint16_t* out;            // fc1: hidden rows [n, rows]; fc2: [tokens, ld]
+  const float* weight;      // fc2: [n] or null
+  const uint16_t* residual; // fc2: [tokens, ld] or null
+  long long ld;
+  int E, topk, rows, K, kw;
+};
+
+// s[0..3] summed over the warp: lane 8 q (and its seven neighbours) get the sum of s[q'], q' = lane / 8 with
+// its bits in the order (16, 8).
+__device__ __forceinline__ float warp_sum4(const float (&s)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool a = lane & 16, b = lane & 8;
+  const float x0 = (a ? s[2] : s[0]) + __shfl_xor_sync(0xffffffffu, a ? s[0] : s[2], 16);
+  const float x1 = (a ? s[3] : s[1]) + __shfl_xor_sync(0xffffffffu, a ? s[1] : s[3], 16);
+  float v = (b ? x1 : x0) + __shfl_xor_sync(0xffffffffu, b ? x0 : x1, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  return v + __shfl_xor_sync(0xffffffffu, v, 1);
+}
+
+template <int V>
+struct VecTile {
+  Chunk<Bf16> w[kVecRows][V];
+  // The piece of rows row0 .. row0 + 3 of expert e's matrix; rows past the last hold zeros.
+  __device__ __forceinline__ void load(const ExpertVec& g, int e, int row0, int first, int end) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) {
+      const uint16_t* from = g.w + ((size_t)e * g.rows + row0 + r) * g.K;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = first + 32 * v + lane;
+        if (row0 + r < g.rows && c < end) chunk_ldg(w[r][v], from + c * 8);
+        else chunk_zero(w[r][v]);
+      }
+    }
+  }
+  // The four rows' products with x (its piece), over the warp: the lane's row as in warp_sum4.
+  __device__ __forceinline__ float dot(const uint16_t* x, int first, int end) const {
+    const int lane = threadIdx.x & 31;
+    uint64_t acc[kVecRows] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = first + 32 * v + lane;
+      Chunk<Bf16> xc;
+      if (c < end) chunk_load(xc, x + c * 8);
+      else chunk_zero(xc);
+      float xf[8], wf[8];
+      chunk_floats(xc, xf);
+#pragma unroll
+      for (int r = 0; r < kVecRows; ++r) {
+        chunk_floats(w[r][v], wf);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          acc[r] = f2_fma(f2_pack(wf[2 * q], wf[2 * q + 1]), f2_pack(xf[2 * q], xf[2 * q + 1]), acc[r]);
+      }
+    }
+    float s[kVecRows];
+#pragma unroll
+    for (int r = 0; r < kVecRows; ++r) {
+      float lo, hi;
+      f2_unpack(acc[r], lo, hi);
+      s[r] = lo + hi;
+    }
+    return warp_sum4(s);
+  }
+};
+
+// The expert of assignment a, or -1 (one out of range is recorded).
+__device__ __forceinline__ int vec_expert(const ExpertVec& g, long long a, int* status) {
+  const int e = __ldg(g.ids + a);
+  if (e < -1 || e >= g.E) {
+    record_bad_index(status);
+    return -1;
+  }
+  return e;
+}
+
+// hidden[a] = GELU(W1_e x[a / topk] + b1_e), rounded to bf16.
+template <int V>
+__global__ void __launch_bounds__(256, 2) k_expert_vec_fc1(const ExpertVec g, int* status) {
+  __shared__ float part[8 * kVecRows][8];   // [row][piece]
+  griddep_wait();
+  griddep_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = g.kw, piece = warp % kw, grp = warp / kw;
+  const int per_block = 8 / kw * kVecRows;
+  const long long a = blockIdx.y;
+  const int e = vec_expert(g, a, status);
+  if (e < 0) return;
+  const int chunks = g.K / 8, per = (chunks + kw - 1) / kw;
+  const int first = piece * per, end = min(chunks, first + per);
+  const int row0 = blockIdx.x * per_block + grp * kVecRows;
+  VecTile<V> tile;
+  tile.load(g, e, row0, first, end);
+  const float v = tile.dot(g.x + a / g.topk * g.ld, first, end);
+  if ((lane & 7) == 0) part[grp * kVecRows + lane / 8][piece] = v;
+  __syncthreads();
+  const int r = threadIdx.x, f = blockIdx.x * per_block + r;
+  if (r >= per_block || f >= g.rows) return;
+  float z = 0.f;
+  for (int q = 0; q < kw; ++q) z += part[r][q];
+  if (g.bias) z += __uint_as_float((uint32_t)__ldg(g.bias + (size_t)e * g.rows + f) << 16);
+  float unused = 0.f;
+  gelu_erf2(z, unused);
+  const __nv_bfloat16 h = __float2bfloat16_rn(z);
+  g.out[a * g.rows + f] = *reinterpret_cast<const uint16_t*>(&h);
+}
+
+// out[t] = residual[t] + sum_j weight[t, j] (W2_e hidden[t, j] + b2_e), the sum in the order of j.
+template <int V>
+__global__ void __launch_bounds__(256, 2) k_expert_vec_fc2(const ExpertVec g, int* status) {
+  __shared__ float part[kMaxTopk][8 * kVecRows][8];   // [expert][row][piece]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int kw = g.kw, piece = warp % kw, grp = warp / kw;
+  const int per_block = 8 / kw * kVecRows;
+  const long long t = blockIdx.y;
+  const int chunks = g.K / 8, per = (chunks + kw - 1) / kw;
+  const int first = piece * per, end = min(chunks, first + per);
+  const int row0 = blockIdx.x * per_block + grp * kVecRows;
+  // ids and weights were final before fc1 began.
+  VecTile<V> tile;
+  int e = vec_expert(g, t * g.topk, status);
+  if (e >= 0) tile.load(g, e, row0, first, end);
+  griddep_wait();
+  griddep_launch();
+  for (int j = 0; j < g.topk; ++j) {
+    const long long a = t * g.topk + j;
+    if (j > 0) {
+      e = vec_expert(g, a, status);
+      if (e >= 0) tile.load(g, e, row0, first, end);
+    }
+    if (e < 0) continue;
+    const float v = tile.dot(g.x + a * g.K, first, end);
+    if ((lane & 7) == 0) part[j][grp * kVecRows + lane / 8][piece] = v;
+  }
+  __syncthreads();
+  const int r = threadIdx.x, c = blockIdx.x * per_block + r;
+  if (r >= per_block || c >= g.rows) return;
+  float acc = 0.f;
+  for (int j = 0; j < g.topk; ++j) {
+    const long long a = t * g.topk + j;
+    const int ej = __ldg(g.ids + a);
+    if (ej < 0 || ej >= g.E) continue;
+    float y = 0.f;
+    for (int q = 0; q < kw; ++q) y += part[j][r][q];
+    if (g.bias) y += __uint_as_float((uint32_t)__ldg(g.bias + (size_t)ej * g.rows + c) << 16);
+    acc += (g.weight ? __ldg(g.weight + a) : 1.f) * y;
+  }
+  if (g.residual) acc += __uint_as_float((uint32_t)g.residual[t * g.ld + c] << 16);
+  const __nv_bfloat16 o = __float2bfloat16_rn(acc);
+  g.out[t * g.ld + c] = *reinterpret_cast<const uint16_t*>(&o);
+}
+
+bool expert_vec_fits(long long n, int C, int hidden) {
+  return n <= kVecMostAssignments && C <= kVecMostK && hidden <= kVecMostK;
+}
+
+// fc1 (fc2 == false: `count` assignments) or fc2 (`count` tokens).
+static cudaError_t launch_vec(ExpertVec g, bool fc2, int count, int* status, cudaStream_t st) {
+  const int chunks = g.K / 8;
+  g.kw = 1;
+  while (g.kw * 128 < chunks) g.kw *= 2;
+  const int v = ((chunks + g.kw - 1) / g.kw + 31) / 32;
+  const int per_block = 8 / g.kw * kVecRows;
+  const dim3 grid((g.rows + per_block - 1) / per_block, count);
+  auto go = [&](auto k1, auto k2) {
+    return launch_pdl(fc2 ? k2 : k1, grid, dim3(256), 0, st, g, status);
+  };
+  switch (v) {
+    case 1: return go(k_expert_vec_fc1<1>, k_expert_vec_fc2<1>);
+    case 2: return go(k_expert_vec_fc1<2>, k_expert_vec_fc2<2>);
+    case 3: return go(k_expert_vec_fc1<3>, k_expert_vec_fc2<3>);
+    default: return go(k_expert_vec_fc1<4>, k_expert_vec_fc2<4>);
+  }
+}
+
+cudaError_t launch_expert_vec_fc1(const uint16_t* x, long long ld, const int32_t* ids,
+                                  const uint16_t* w1, const uint16_t* b1, uint16_t* h, int n,
+                                  int topk, int E, int C, int hidden, int* status,
+                                  cudaStream_t st) {
+  ExpertVec g = {};
+  g.x = x;
+  g.ids = ids;
+  g.w = w1;
+  g.bias = b1;
+  g.out = h;
+  g.ld = ld;
+  g.E = E;
+  g.topk = topk;
+  g.rows = hidden;
+  g.K = C;
+  return launch_vec(g, false, n, status, st);
+}
+
+cudaError_t launch_expert_vec_fc2(const uint16_t* h, const int32_t* ids, const float* weight,
+                                  const uint16_t* residual, const uint16_t* w2,
+                                  const uint16_t* b2, uint16_t* out, long long ld, int tokens,
+                                  int topk, int E, int C, int hidden, int* status,
+                                  cudaStream_t st) {
+  ExpertVec g = {};
+  g.x = h;
+  g.ids = ids;
+  g.w = w2;
+  g.bias = b2;
+  g.out = out;
+  g.weight = weight;
+  g.residual = residual;
+  g.ld = ld;
+  g.E = E;
+  g.topk = topk;
+  g.rows = C;
+  g.K = hidden;
+  return launch_vec(g, true, tokens, status, st);
+}
+
+}  // namespace ss

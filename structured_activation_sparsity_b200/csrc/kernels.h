@@ -17,7 +17,6 @@ constexpr int kMaxRankTokens = 16384;   // tokens per unit the rank kernel holds
 cudaError_t set_wait_limit_attn(uint64_t ns);
 cudaError_t set_wait_limit_mlp(uint64_t ns);
 cudaError_t set_wait_limit_norm(uint64_t ns);
-cudaError_t set_wait_limit_expert_mlp(uint64_t ns);
 
 // sparsesam_rcmlp's argument checks (same codes, same order) and its workspace bytes in *need.
 int rcmlp_validate(const ss_cfg* cfg, const uint16_t* x, int32_t C, int32_t hidden,
@@ -288,5 +287,16 @@ ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool s
 cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
                                const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
                                cudaStream_t st);
+
+// The same MLP for a few assignments, straight from the unsorted tokens (see expert_mlp.cuh).
+constexpr int kVecMostAssignments = 8;
+bool expert_vec_fits(long long n, int C, int hidden);
+cudaError_t launch_expert_vec_fc1(const uint16_t* x, long long ld, const int32_t* ids,
+                                  const uint16_t* w1, const uint16_t* b1, uint16_t* h, int n,
+                                  int topk, int E, int C, int hidden, int* status, cudaStream_t st);
+cudaError_t launch_expert_vec_fc2(const uint16_t* h, const int32_t* ids, const float* weight,
+                                  const uint16_t* residual, const uint16_t* w2,
+                                  const uint16_t* b2, uint16_t* out, long long ld, int tokens,
+                                  int topk, int E, int C, int hidden, int* status, cudaStream_t st);
 
 }  // namespace ss

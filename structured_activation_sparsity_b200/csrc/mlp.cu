@@ -693,3 +693,5 @@ cudaError_t launch_gemm(const CUtensorMap* ta, const CUtensorMap* tb, const Gemm
 cudaError_t set_wait_limit_mlp(uint64_t ns) { return set_wait_limit_here(ns); }
 
 }  // namespace ss
+
+#include "expert_mlp.cuh"
