@@ -354,21 +354,21 @@ int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int3
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (expert_vec_fits(n, C, H)) {
     rc = cuda_err(traced("expert_vec_fc1", st, [&] {
-      return launch_expert_vec_fc1(x, or_C(cfg->ld, C), ids, w1, b1, h, n, cfg->topk, E, C, H,
-                                   status, st);
+      return launch_expert_vec(false, x, or_C(cfg->ld, C), ids, nullptr, nullptr, w1, b1, h, n,
+                               cfg->topk, E, H, C, status, st);
     }));
     if (rc) return rc;
     return cuda_err(traced("expert_vec_fc2", st, [&] {
-      return launch_expert_vec_fc2(h, ids, weight, residual, w2, b2, out, or_C(cfg->ld, C),
-                                   cfg->tokens, cfg->topk, E, C, H, status, st);
+      return launch_expert_vec(true, h, or_C(cfg->ld, C), ids, weight, residual, w2, b2, out, n,
+                               cfg->topk, E, C, H, status, st);
     }));
   }
   CUtensorMap tw1, tx, tw2, th;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_bf16(&tw1, 2, w1, C, (uint64_t)E * H, 1, (uint64_t)C * 2, 64, 128, sw) ||
-      !encode_bf16(&tx, 2, xs, C, n, 1, (uint64_t)C * 2, 64, L.fc1.tn, sw) ||
+      !encode_bf16(&tx, 2, xs, C, n, 1, (uint64_t)C * 2, 64, expert_box(L.fc1.tn), sw) ||
       !encode_bf16(&tw2, 2, w2, H, (uint64_t)E * C, 1, (uint64_t)H * 2, 64, 128, sw) ||
-      !encode_bf16(&th, 2, h, H, n, 1, (uint64_t)H * 2, 64, L.fc2.tn, sw))
+      !encode_bf16(&th, 2, h, H, n, 1, (uint64_t)H * 2, 64, expert_box(L.fc2.tn), sw))
     return SS_ECUDA;
   if ((rc = sort_launch(ids, nullptr, slot, offsets, n, E, wsb + L.sort, status, st))) return rc;
   rc = cuda_err(traced("expert_gather", st, [&] {

@@ -29,9 +29,11 @@ static_assert(128 * kXRegsProducer + 256 * kXRegsEpilogue <= 384 * 168,
 // in 2 KB of shared memory: 64 bytes a row, so that it stores 16 bytes a lane, eight rows an instruction.
 constexpr int kXTurn = 32 * 64;
 
-// Token tile TN: a stage holds one 64-wide k-block of 128 weight rows and TN token rows.
+// Token tile TN: a stage holds one 64-wide k-block of 128 weight rows and up to TN token rows, which come
+// in boxes of kBox rows, as many as the tile has rows for.
 template <int TN>
 struct XCfg {
+  static constexpr int kBox = expert_box(TN);
   static constexpr int kABytes = 128 * 128;
   static constexpr int kBBytes = TN * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
@@ -142,16 +144,18 @@ __global__ void __launch_bounds__(kXThreads, 1)
       bool ok = true;
       for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
         const XUnit r = decode(u);
-        const int nk = r.kb1 - r.kb0;
+        const int nk = r.kb1 - r.kb0, boxes = (r.rows + G::kBox - 1) / G::kBox;
         for (int j = 0; j < nk; ++j, ++it) {
           const int st = it % G::kStages;
           if (it >= G::kStages &&
               !(ok = mbar_wait(empty + st, ((it / G::kStages) - 1) & 1, abort, status)))
             break;
           uint8_t* sa = smem + st * G::kStageBytes;
-          mbar_expect_tx(full + st, G::kStageBytes);
+          mbar_expect_tx(full + st, G::kABytes + boxes * G::kBox * 128);
           tma_load_2d(sa, &ta, full + st, (r.kb0 + j) * 64, r.e * g.features + r.m0);
-          tma_load_2d(sa + G::kABytes, &tb, full + st, (r.kb0 + j) * 64, r.row0);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d(sa + G::kABytes + b * G::kBox * 128, &tb, full + st, (r.kb0 + j) * 64,
+                        r.row0 + b * G::kBox);
         }
       }
     } else if (warp == 1 && lane == 0) {
@@ -253,9 +257,11 @@ __global__ void __launch_bounds__(kXThreads, 1)
 ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms) {
   ExpertGemmPlan p;
   p.m_tiles = (features + 127) / 128;
-  // The narrowest token tile that holds an average expert's rows.
+  // A token tile of twice an average expert's rows: an expert with one row more than the tile reads its
+  // weights again for a second one (784 tokens over 16 experts, 98 rows on average: 98 us with tiles of
+  // 128, 87 us with 256), while what a tile does not fill is not loaded.
   const long long avg = (n + E - 1) / E;
-  p.tn = avg <= 32 ? 32 : avg <= 64 ? 64 : avg <= 128 ? 128 : 256;
+  p.tn = avg <= 32 ? 64 : avg <= 64 ? 128 : 256;
   // Tiles at most: one per expert with rows, and one more per full tile.
   long long tiles = n / p.tn + (n < E ? n : E);
   if (tiles > n) tiles = n;
@@ -285,7 +291,6 @@ cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
                                cudaStream_t st) {
   const int grid = (int)(p.max_units < sms ? p.max_units : sms);
   switch (p.tn) {
-    case 32: return launch_x<32>(ta, tb, g, grid, status, st);
     case 64: return launch_x<64>(ta, tb, g, grid, status, st);
     case 128: return launch_x<128>(ta, tb, g, grid, status, st);
     default: return launch_x<256>(ta, tb, g, grid, status, st);
@@ -293,14 +298,16 @@ cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
 }
 
 // ---- few rows -----------------------------------------------------------------------------------
-// A handful of assignments (single tokens) read an expert's weights for one row each, and that is all that
-// counts: 2 C hidden bf16 an assignment. Two launches without sort or gather: fc1 over (features,
-// assignments), fc2 over (channels, tokens), which also weights and adds the token's experts and its
-// residual. A block's eight warps are `kw` pieces of the product's K times 8 / kw groups of four weight rows;
-// a warp has its piece of all four rows (4 V 16-byte loads a lane) in flight at once. fc2 requests its first
-// weights before it waits for fc1.
+// A handful of assignments read an expert's weights for one row each, and that is all that counts: 2 C
+// hidden bf16 an assignment. Two launches without sort or gather: fc1 over (features, assignments), fc2
+// over (channels, tokens), which also weights and adds the token's experts and its residual. A warp has
+// four weight rows (fc2: two channels of two experts), or its span of them where several warps share
+// long rows, in flight at once: up to twenty 16-byte loads a lane and no loop, so that a token of two
+// experts at ViT-H widths is on its way from HBM whole, in one wave of blocks, a microsecond after the
+// launch. fc2 requests its first weights before it waits for fc1.
 constexpr int kVecRows = 4;                    // weight rows of a warp
-constexpr int kVecMostK = 8 * 32 * 4 * 8;      // longest K: eight warps of four chunks a lane
+constexpr int kVecSpan = 5;                    // chunks a lane of each, at most
+constexpr int kVecMostK = 8 * 32 * kVecSpan * 8;
 
 struct ExpertVec {
   const uint16_t* x;        // fc1: [tokens, ld]; fc2: hidden rows [n, K]
@@ -310,11 +317,11 @@ struct ExpertVec {
   const float* weight;      // fc2: [n] or null
   const uint16_t* residual; // fc2: [tokens, ld] or null
   long long ld;
-  int E, topk, rows, K, kw;
+  int E, topk, rows, K;
+  int kw;                   // warps that share a row's K
 };
 
-// s[0..3] summed over the warp: lane 8 q (and its seven neighbours) get the sum of s[q'], q' = lane / 8 with
-// its bits in the order (16, 8).
+// s[0..3] summed over the warp: lane 8 q (and its seven neighbours) get the sum of s[q].
 __device__ __forceinline__ float warp_sum4(const float (&s)[4]) {
   const int lane = threadIdx.x & 31;
   const bool a = lane & 16, b = lane & 8;
@@ -329,38 +336,52 @@ __device__ __forceinline__ float warp_sum4(const float (&s)[4]) {
 template <int V>
 struct VecTile {
   Chunk<Bf16> w[kVecRows][V];
-  // The piece of rows row0 .. row0 + 3 of expert e's matrix; rows past the last hold zeros.
-  __device__ __forceinline__ void load(const ExpertVec& g, int e, int row0, int first, int end) {
+  // The span [first, end) of rows row0 .. row0 + ROWS - 1 of expert e's matrix into w[at ..]; zeros for rows
+  // past the last, or without an expert.
+  template <int ROWS>
+  __device__ __forceinline__ void load(const ExpertVec& g, int e, int row0, int first, int end,
+                                       int at) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int r = 0; r < kVecRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       const uint16_t* from = g.w + ((size_t)e * g.rows + row0 + r) * g.K;
+      const bool live = e >= 0 && row0 + r < g.rows;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const int c = first + 32 * v + lane;
-        if (row0 + r < g.rows && c < end) chunk_ldg(w[r][v], from + c * 8);
-        else chunk_zero(w[r][v]);
+        if (live && c < end) chunk_ldg(w[at + r][v], from + c * 8);
+        else chunk_zero(w[at + r][v]);
       }
     }
   }
-  // The four rows' products with x (its piece), over the warp: the lane's row as in warp_sum4.
-  __device__ __forceinline__ float dot(const uint16_t* x, int first, int end) const {
+  // The products of w[0], w[1] with x0 and of w[2], w[3] with x1 (their spans), over the warp: the lane's
+  // as in warp_sum4.
+  template <bool SAME>
+  __device__ __forceinline__ float dot(const uint16_t* x0, const uint16_t* x1, int first,
+                                       int end) const {
     const int lane = threadIdx.x & 31;
     uint64_t acc[kVecRows] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int c = first + 32 * v + lane;
-      Chunk<Bf16> xc;
-      if (c < end) chunk_load(xc, x + c * 8);
-      else chunk_zero(xc);
-      float xf[8], wf[8];
-      chunk_floats(xc, xf);
+      Chunk<Bf16> xc[2];
+      chunk_zero(xc[0]);
+      chunk_zero(xc[1]);
+      if (c < end) {
+        chunk_load(xc[0], x0 + c * 8);
+        if (!SAME) chunk_load(xc[1], x1 + c * 8);
+      }
+      float xf[2][8], wf[8];
+      chunk_floats(xc[0], xf[0]);
+      if (!SAME) chunk_floats(xc[1], xf[1]);
 #pragma unroll
       for (int r = 0; r < kVecRows; ++r) {
+        const int h = SAME ? 0 : r / 2;
         chunk_floats(w[r][v], wf);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          acc[r] = f2_fma(f2_pack(wf[2 * q], wf[2 * q + 1]), f2_pack(xf[2 * q], xf[2 * q + 1]), acc[r]);
+          acc[r] = f2_fma(f2_pack(wf[2 * q], wf[2 * q + 1]), f2_pack(xf[h][2 * q], xf[h][2 * q + 1]),
+                          acc[r]);
       }
     }
     float s[kVecRows];
@@ -383,16 +404,20 @@ __device__ __forceinline__ int vec_expert(const ExpertVec& g, long long a, int* 
   }
   return e;
 }
+__device__ __forceinline__ float vec_bias(const ExpertVec& g, int e, int row) {
+  return g.bias ? __uint_as_float((uint32_t)__ldg(g.bias + (size_t)e * g.rows + row) << 16) : 0.f;
+}
 
-// hidden[a] = GELU(W1_e x[a / topk] + b1_e), rounded to bf16.
-template <int V>
-__global__ void __launch_bounds__(256, 2) k_expert_vec_fc1(const ExpertVec g, int* status) {
-  __shared__ float part[8 * kVecRows][8];   // [row][piece]
+// hidden[a] = GELU(W1_e x[a / topk] + b1_e), rounded to bf16. WARPS of a block: kw a group of four features.
+template <int V, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+    k_expert_vec_fc1(const ExpertVec g, int* status) {
+  __shared__ float part[WARPS * kVecRows][WARPS];   // [row][piece]
   griddep_wait();
   griddep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kw = g.kw, piece = warp % kw, grp = warp / kw;
-  const int per_block = 8 / kw * kVecRows;
+  const int per_block = WARPS / kw * kVecRows;
   const long long a = blockIdx.y;
   const int e = vec_expert(g, a, status);
   if (e < 0) return;
@@ -400,15 +425,16 @@ __global__ void __launch_bounds__(256, 2) k_expert_vec_fc1(const ExpertVec g, in
   const int first = piece * per, end = min(chunks, first + per);
   const int row0 = blockIdx.x * per_block + grp * kVecRows;
   VecTile<V> tile;
-  tile.load(g, e, row0, first, end);
-  const float v = tile.dot(g.x + a / g.topk * g.ld, first, end);
+  tile.template load<kVecRows>(g, e, row0, first, end, 0);
+  const int r = threadIdx.x, f = blockIdx.x * per_block + r;
+  const bool mine = r < per_block && f < g.rows;
+  float z = mine ? vec_bias(g, e, f) : 0.f;
+  const uint16_t* x = g.x + a / g.topk * g.ld;
+  const float v = tile.template dot<true>(x, x, first, end);
   if ((lane & 7) == 0) part[grp * kVecRows + lane / 8][piece] = v;
   __syncthreads();
-  const int r = threadIdx.x, f = blockIdx.x * per_block + r;
-  if (r >= per_block || f >= g.rows) return;
-  float z = 0.f;
+  if (!mine) return;
   for (int q = 0; q < kw; ++q) z += part[r][q];
-  if (g.bias) z += __uint_as_float((uint32_t)__ldg(g.bias + (size_t)e * g.rows + f) << 16);
   float unused = 0.f;
   gelu_erf2(z, unused);
   const __nv_bfloat16 h = __float2bfloat16_rn(z);
@@ -416,47 +442,55 @@ __global__ void __launch_bounds__(256, 2) k_expert_vec_fc1(const ExpertVec g, in
 }
 
 // out[t] = residual[t] + sum_j weight[t, j] (W2_e hidden[t, j] + b2_e), the sum in the order of j.
-template <int V>
-__global__ void __launch_bounds__(256, 2) k_expert_vec_fc2(const ExpertVec g, int* status) {
-  __shared__ float part[kMaxTopk][8 * kVecRows][8];   // [expert][row][piece]
+template <int V, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+    k_expert_vec_fc2(const ExpertVec g, int* status) {
+  constexpr int kRows = kVecRows / 2;                      // channels of a warp
+  __shared__ float part[kMaxTopk][WARPS * kRows][WARPS];   // [expert][row][piece]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kw = g.kw, piece = warp % kw, grp = warp / kw;
-  const int per_block = 8 / kw * kVecRows;
+  const int per_block = WARPS / kw * kRows;
   const long long t = blockIdx.y;
   const int chunks = g.K / 8, per = (chunks + kw - 1) / kw;
   const int first = piece * per, end = min(chunks, first + per);
-  const int row0 = blockIdx.x * per_block + grp * kVecRows;
-  // ids and weights were final before fc1 began.
+  const int row0 = blockIdx.x * per_block + grp * kRows;
+  const int r = threadIdx.x, c = blockIdx.x * per_block + r;
+  const bool mine = r < per_block && c < g.rows;
   VecTile<V> tile;
-  int e = vec_expert(g, t * g.topk, status);
-  if (e >= 0) tile.load(g, e, row0, first, end);
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int e = j0 + q < g.topk ? vec_expert(g, t * g.topk + j0 + q, status) : -1;
+      tile.template load<kRows>(g, e, row0, first, end, q * kRows);
+    }
+  };
+  // ids and weights were final before fc1 began.
+  load(0);
   griddep_wait();
   griddep_launch();
-  for (int j = 0; j < g.topk; ++j) {
-    const long long a = t * g.topk + j;
-    if (j > 0) {
-      e = vec_expert(g, a, status);
-      if (e >= 0) tile.load(g, e, row0, first, end);
-    }
-    if (e < 0) continue;
-    const float v = tile.dot(g.x + a * g.K, first, end);
-    if ((lane & 7) == 0) part[j][grp * kVecRows + lane / 8][piece] = v;
+  const float res =
+      g.residual && mine ? __uint_as_float((uint32_t)g.residual[t * g.ld + c] << 16) : 0.f;
+  for (int j0 = 0; j0 < g.topk; j0 += 2) {
+    if (j0 > 0) load(j0);
+    const long long a = t * g.topk + j0;
+    const float v = tile.template dot<false>(
+        g.x + a * g.K, g.x + (j0 + 1 < g.topk ? a + 1 : a) * g.K, first, end);
+    const int q = lane >> 4;   // warp_sum4: rows 0, 1 are expert j0's, 2 and 3 the next one's
+    if ((lane & 7) == 0 && j0 + q < g.topk)
+      part[j0 + q][grp * kRows + ((lane >> 3) & 1)][piece] = v;
   }
   __syncthreads();
-  const int r = threadIdx.x, c = blockIdx.x * per_block + r;
-  if (r >= per_block || c >= g.rows) return;
+  if (!mine) return;
   float acc = 0.f;
   for (int j = 0; j < g.topk; ++j) {
     const long long a = t * g.topk + j;
-    const int ej = __ldg(g.ids + a);
-    if (ej < 0 || ej >= g.E) continue;
+    const int e = __ldg(g.ids + a);
+    if (e < 0 || e >= g.E) continue;
     float y = 0.f;
     for (int q = 0; q < kw; ++q) y += part[j][r][q];
-    if (g.bias) y += __uint_as_float((uint32_t)__ldg(g.bias + (size_t)ej * g.rows + c) << 16);
-    acc += (g.weight ? __ldg(g.weight + a) : 1.f) * y;
+    acc += (g.weight ? __ldg(g.weight + a) : 1.f) * (y + vec_bias(g, e, c));
   }
-  if (g.residual) acc += __uint_as_float((uint32_t)g.residual[t * g.ld + c] << 16);
-  const __nv_bfloat16 o = __float2bfloat16_rn(acc);
+  const __nv_bfloat16 o = __float2bfloat16_rn(acc + res);
   g.out[t * g.ld + c] = *reinterpret_cast<const uint16_t*>(&o);
 }
 
@@ -464,62 +498,44 @@ bool expert_vec_fits(long long n, int C, int hidden) {
   return n <= kVecMostAssignments && C <= kVecMostK && hidden <= kVecMostK;
 }
 
-// fc1 (fc2 == false: `count` assignments) or fc2 (`count` tokens).
-static cudaError_t launch_vec(ExpertVec g, bool fc2, int count, int* status, cudaStream_t st) {
-  const int chunks = g.K / 8;
-  g.kw = 1;
-  while (g.kw * 128 < chunks) g.kw *= 2;
-  const int v = ((chunks + g.kw - 1) / g.kw + 31) / 32;
-  const int per_block = 8 / g.kw * kVecRows;
-  const dim3 grid((g.rows + per_block - 1) / per_block, count);
-  auto go = [&](auto k1, auto k2) {
-    return launch_pdl(fc2 ? k2 : k1, grid, dim3(256), 0, st, g, status);
-  };
-  switch (v) {
-    case 1: return go(k_expert_vec_fc1<1>, k_expert_vec_fc2<1>);
-    case 2: return go(k_expert_vec_fc1<2>, k_expert_vec_fc2<2>);
-    case 3: return go(k_expert_vec_fc1<3>, k_expert_vec_fc2<3>);
-    default: return go(k_expert_vec_fc1<4>, k_expert_vec_fc2<4>);
-  }
-}
-
-cudaError_t launch_expert_vec_fc1(const uint16_t* x, long long ld, const int32_t* ids,
-                                  const uint16_t* w1, const uint16_t* b1, uint16_t* h, int n,
-                                  int topk, int E, int C, int hidden, int* status,
-                                  cudaStream_t st) {
+cudaError_t launch_expert_vec(bool fc2, const uint16_t* x, long long ld, const int32_t* ids,
+                              const float* weight, const uint16_t* residual, const uint16_t* w,
+                              const uint16_t* bias, uint16_t* out, int n, int topk, int E, int rows,
+                              int K, int* status, cudaStream_t st) {
   ExpertVec g = {};
   g.x = x;
   g.ids = ids;
-  g.w = w1;
-  g.bias = b1;
-  g.out = h;
-  g.ld = ld;
-  g.E = E;
-  g.topk = topk;
-  g.rows = hidden;
-  g.K = C;
-  return launch_vec(g, false, n, status, st);
-}
-
-cudaError_t launch_expert_vec_fc2(const uint16_t* h, const int32_t* ids, const float* weight,
-                                  const uint16_t* residual, const uint16_t* w2,
-                                  const uint16_t* b2, uint16_t* out, long long ld, int tokens,
-                                  int topk, int E, int C, int hidden, int* status,
-                                  cudaStream_t st) {
-  ExpertVec g = {};
-  g.x = h;
-  g.ids = ids;
-  g.w = w2;
-  g.bias = b2;
+  g.w = w;
+  g.bias = bias;
   g.out = out;
   g.weight = weight;
   g.residual = residual;
   g.ld = ld;
   g.E = E;
   g.topk = topk;
-  g.rows = C;
-  g.K = hidden;
-  return launch_vec(g, true, tokens, status, st);
+  g.rows = rows;
+  g.K = K;
+  // The fewest warps a row, which leave the fewest lanes without a chunk.
+  const int chunks = K / 8;
+  g.kw = 1;
+  while (g.kw * 32 * kVecSpan < chunks) g.kw *= 2;
+  const int v = ((chunks + g.kw - 1) / g.kw + 31) / 32, warps = g.kw > 4 ? 8 : 4;
+  const int per_block = warps / g.kw * (fc2 ? kVecRows / 2 : kVecRows);
+  const dim3 grid((rows + per_block - 1) / per_block, fc2 ? n / topk : n);
+  auto go = [&](auto k1, auto k2) {
+    return launch_pdl(fc2 ? k2 : k1, grid, dim3(warps * 32), 0, st, g, status);
+  };
+  if (warps == 8) {
+    if (v <= 3) return go(k_expert_vec_fc1<3, 8>, k_expert_vec_fc2<3, 8>);
+    return go(k_expert_vec_fc1<5, 8>, k_expert_vec_fc2<5, 8>);
+  }
+  switch (v) {
+    case 1: return go(k_expert_vec_fc1<1, 4>, k_expert_vec_fc2<1, 4>);
+    case 2: return go(k_expert_vec_fc1<2, 4>, k_expert_vec_fc2<2, 4>);
+    case 3: return go(k_expert_vec_fc1<3, 4>, k_expert_vec_fc2<3, 4>);
+    case 4: return go(k_expert_vec_fc1<4, 4>, k_expert_vec_fc2<4, 4>);
+    default: return go(k_expert_vec_fc1<5, 4>, k_expert_vec_fc2<5, 4>);
+  }
 }
 
 }  // namespace ss

@@ -283,20 +283,22 @@ struct ExpertGemmPlan {
   long long max_units;       // at most
 };
 ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms);
-// ta: weights [E * features, Kd], box 128 rows; tb: rows [n, Kd], box p.tn rows; both 64 columns.
+// Rows of a token box of a tile of tn rows.
+__host__ __device__ constexpr int expert_box(int tn) { return tn < 256 ? 32 : 64; }
+// ta: weights [E * features, Kd], box 128 rows; tb: rows [n, Kd], box expert_box(p.tn) rows; both 64
+// columns.
 cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
                                const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
                                cudaStream_t st);
 
-// The same MLP for a few assignments, straight from the unsorted tokens (see expert_mlp.cuh).
+// The products of a few assignments, straight from the unsorted tokens (see expert_mlp.cuh): fc1 (x [tokens,
+// ld], weights [E, rows, K] -> out: the hidden rows [n, rows]) or fc2 (x: the hidden rows [n, K] -> out
+// [tokens, ld], weighted, with the residual).
 constexpr int kVecMostAssignments = 8;
 bool expert_vec_fits(long long n, int C, int hidden);
-cudaError_t launch_expert_vec_fc1(const uint16_t* x, long long ld, const int32_t* ids,
-                                  const uint16_t* w1, const uint16_t* b1, uint16_t* h, int n,
-                                  int topk, int E, int C, int hidden, int* status, cudaStream_t st);
-cudaError_t launch_expert_vec_fc2(const uint16_t* h, const int32_t* ids, const float* weight,
-                                  const uint16_t* residual, const uint16_t* w2,
-                                  const uint16_t* b2, uint16_t* out, long long ld, int tokens,
-                                  int topk, int E, int C, int hidden, int* status, cudaStream_t st);
+cudaError_t launch_expert_vec(bool fc2, const uint16_t* x, long long ld, const int32_t* ids,
+                              const float* weight, const uint16_t* residual, const uint16_t* w,
+                              const uint16_t* bias, uint16_t* out, int n, int topk, int E, int rows,
+                              int K, int* status, cudaStream_t st);
 
 }  // namespace ss
