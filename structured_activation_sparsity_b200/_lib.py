@@ -146,6 +146,11 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _ptrs(*tensors):
+    """_ptr of each (one pass: a call of a dozen pointers is on the path of small launches)."""
+    return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
+
+
 def _stream(stream) -> int | None:
     if stream is None:
         return None
@@ -360,11 +365,9 @@ def make_expert_cfg(tokens, experts, topk, C=0, hidden=0, dtype="bf16", ld=0) ->
 def sparsesam_norm_residual(cfg, y, x, gate, scale, post_w, post_b, pre_w, pre_b, x_out, n, stats,
                             stream=None):
     """x_out = x + gate * scale * post norm(y), n = pre norm(x_out); absent parameters are None."""
-    return _check("sparsesam_norm_residual",
-                  lib.sparsesam_norm_residual(ctypes.byref(cfg), _ptr(y), _ptr(x), _ptr(gate),
-                                              _ptr(scale), _ptr(post_w), _ptr(post_b),
-                                              _ptr(pre_w), _ptr(pre_b), _ptr(x_out), _ptr(n),
-                                              _ptr(stats), _stream(stream)))
+    return _check("sparsesam_norm_residual", lib.sparsesam_norm_residual(
+        ctypes.byref(cfg), *_ptrs(y, x, gate, scale, post_w, post_b, pre_w, pre_b, x_out, n, stats),
+        _stream(stream)))
 
 
 def sparsesam_norm_residual_backward_workspace(cfg) -> int:
@@ -375,27 +378,23 @@ def sparsesam_norm_residual_backward(cfg, y, x_out, gate, scale, post_w, post_b,
                                      dx_out, dn, dx, dy, dgate, dscale, dpost_w, dpost_b, dpre_w,
                                      dpre_b, ws, ws_bytes, stream=None):
     """Row gradients dx, dy and the parameters' fp32 gradients (None: not wanted)."""
-    return _check("sparsesam_norm_residual_backward",
-                  lib.sparsesam_norm_residual_backward(
-                      ctypes.byref(cfg), _ptr(y), _ptr(x_out), _ptr(gate), _ptr(scale),
-                      _ptr(post_w), _ptr(post_b), _ptr(pre_w), _ptr(stats), _ptr(dx_out), _ptr(dn),
-                      _ptr(dx), _ptr(dy), _ptr(dgate), _ptr(dscale), _ptr(dpost_w), _ptr(dpost_b),
-                      _ptr(dpre_w), _ptr(dpre_b), _ptr(ws), int(ws_bytes), _stream(stream)))
+    return _check("sparsesam_norm_residual_backward", lib.sparsesam_norm_residual_backward(
+        ctypes.byref(cfg), *_ptrs(y, x_out, gate, scale, post_w, post_b, pre_w, stats, dx_out, dn,
+                                  dx, dy, dgate, dscale, dpost_w, dpost_b, dpre_w, dpre_b, ws),
+        ws_bytes, _stream(stream)))
 
 
 def sparsesam_expert_route(cfg, logits, renorm, ids, weight, stream=None):
     """The topk experts of each token and their softmax weights (renorm: over the chosen only)."""
-    return _check("sparsesam_expert_route",
-                  lib.sparsesam_expert_route(ctypes.byref(cfg), _ptr(logits), int(renorm),
-                                             _ptr(ids), _ptr(weight), _stream(stream)))
+    return _check("sparsesam_expert_route", lib.sparsesam_expert_route(
+        ctypes.byref(cfg), _ptr(logits), int(renorm), *_ptrs(ids, weight), _stream(stream)))
 
 
 def sparsesam_expert_route_backward(cfg, logits, renorm, ids, weight, dweight, dlogits,
                                     stream=None):
-    return _check("sparsesam_expert_route_backward",
-                  lib.sparsesam_expert_route_backward(ctypes.byref(cfg), _ptr(logits), int(renorm),
-                                                      _ptr(ids), _ptr(weight), _ptr(dweight),
-                                                      _ptr(dlogits), _stream(stream)))
+    return _check("sparsesam_expert_route_backward", lib.sparsesam_expert_route_backward(
+        ctypes.byref(cfg), _ptr(logits), int(renorm), *_ptrs(ids, weight, dweight, dlogits),
+        _stream(stream)))
 
 
 def sparsesam_expert_sort_workspace(cfg) -> int:
@@ -404,32 +403,25 @@ def sparsesam_expert_sort_workspace(cfg) -> int:
 
 def sparsesam_expert_sort(cfg, ids, order, slot, offsets, ws, ws_bytes, stream=None):
     """The assignments in a stable order by expert (order, slot, offsets: None to skip one)."""
-    return _check("sparsesam_expert_sort",
-                  lib.sparsesam_expert_sort(ctypes.byref(cfg), _ptr(ids), _ptr(order), _ptr(slot),
-                                            _ptr(offsets), _ptr(ws), int(ws_bytes),
-                                            _stream(stream)))
+    return _check("sparsesam_expert_sort", lib.sparsesam_expert_sort(
+        ctypes.byref(cfg), *_ptrs(ids, order, slot, offsets, ws), ws_bytes, _stream(stream)))
 
 
 def sparsesam_expert_gather(cfg, x, slot, xs, stream=None):
     """xs[slot[t, j]] = x[t]; its gradient is sparsesam_expert_combine without weights."""
-    return _check("sparsesam_expert_gather",
-                  lib.sparsesam_expert_gather(ctypes.byref(cfg), _ptr(x), _ptr(slot), _ptr(xs),
-                                              _stream(stream)))
+    return _check("sparsesam_expert_gather", lib.sparsesam_expert_gather(
+        ctypes.byref(cfg), *_ptrs(x, slot, xs), _stream(stream)))
 
 
 def sparsesam_expert_combine(cfg, ys, slot, weight, residual, out, stream=None):
     """out[t] = residual[t] + sum_j weight[t, j] * ys[slot[t, j]] (None: weights 1, residual 0)."""
-    return _check("sparsesam_expert_combine",
-                  lib.sparsesam_expert_combine(ctypes.byref(cfg), _ptr(ys), _ptr(slot),
-                                               _ptr(weight), _ptr(residual), _ptr(out),
-                                               _stream(stream)))
+    return _check("sparsesam_expert_combine", lib.sparsesam_expert_combine(
+        ctypes.byref(cfg), *_ptrs(ys, slot, weight, residual, out), _stream(stream)))
 
 
 def sparsesam_expert_combine_backward(cfg, dout, ys, slot, weight, dys, dweight, stream=None):
-    return _check("sparsesam_expert_combine_backward",
-                  lib.sparsesam_expert_combine_backward(ctypes.byref(cfg), _ptr(dout), _ptr(ys),
-                                                        _ptr(slot), _ptr(weight), _ptr(dys),
-                                                        _ptr(dweight), _stream(stream)))
+    return _check("sparsesam_expert_combine_backward", lib.sparsesam_expert_combine_backward(
+        ctypes.byref(cfg), *_ptrs(dout, ys, slot, weight, dys, dweight), _stream(stream)))
 
 
 def sparsesam_expert_mlp_workspace(cfg) -> int:
@@ -439,10 +431,9 @@ def sparsesam_expert_mlp_workspace(cfg) -> int:
 def sparsesam_expert_mlp(cfg, x, ids, weight, residual, w1, b1, w2, b2, out, ws, ws_bytes,
                          stream=None):
     """The routed-expert MLP over tokens x with the router's ids and weights."""
-    return _check("sparsesam_expert_mlp",
-                  lib.sparsesam_expert_mlp(ctypes.byref(cfg), _ptr(x), _ptr(ids), _ptr(weight),
-                                           _ptr(residual), _ptr(w1), _ptr(b1), _ptr(w2), _ptr(b2),
-                                           _ptr(out), _ptr(ws), int(ws_bytes), _stream(stream)))
+    return _check("sparsesam_expert_mlp", lib.sparsesam_expert_mlp(
+        ctypes.byref(cfg), *_ptrs(x, ids, weight, residual, w1, b1, w2, b2, out, ws), ws_bytes,
+        _stream(stream)))
 
 
 def sparsesam_set_wait_limit_ns(ns: int):

@@ -256,6 +256,28 @@ size_t rcmlp_ws_bytes(const Geo& g, int K, int C, int hidden) {
 
 }  // namespace
 
+cudaError_t allow_smem(const void* kernel, int bytes) {
+  struct Allowed {
+    const void* kernel;
+    int bytes;
+  };
+  constexpr int kMost = 64;   // kernels remembered a device; any further one is asked for every time
+  static Allowed allowed[128][kMost] = {};
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(g_mu);
+  Allowed* a = allowed[dev];
+  int i = 0;
+  while (i < kMost && a[i].kernel && a[i].kernel != kernel) ++i;
+  if (i < kMost && a[i].kernel && a[i].bytes >= bytes) return cudaSuccess;
+  const cudaError_t s =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (s == cudaSuccess && i < kMost) a[i] = Allowed{kernel, bytes};
+  return s;
+}
+
 int sm_count() {
   static int cached[128] = {};
   int dev = 0;

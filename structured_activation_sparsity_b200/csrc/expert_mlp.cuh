@@ -279,8 +279,7 @@ template <int TN>
 static cudaError_t launch_x(const CUtensorMap* ta, const CUtensorMap* tb, const ExpertGemm& g,
                             int grid, int* status, cudaStream_t st) {
   using G = XCfg<TN>;
-  cudaError_t e = cudaFuncSetAttribute(k_expert_gemm<TN>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, G::kAlloc);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_expert_gemm<TN>), G::kAlloc);
   if (e != cudaSuccess) return e;
   return launch_pdl(k_expert_gemm<TN>, dim3(grid), dim3(kXThreads), G::kAlloc, st, *ta, *tb, g,
                     status);

@@ -13,37 +13,26 @@
 namespace ss {
 
 // ---- router ---------------------------------------------------------------------------------
-// Floats in an order that unsigned integers keep: larger float, larger key. -inf and NaN (a closed
-// expert) give key 0, which no other float has.
-__device__ __forceinline__ uint32_t rank_key(float v) {
-  if (!(v > -INFINITY)) return 0u;
-  const uint32_t u = __float_as_uint(v + 0.0f);   // -0.0 ties with +0.0
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
-}
+// A logit as it ranks: NaN closes its expert like -inf. -0.0 compares equal to +0.0, so they tie.
+__device__ __forceinline__ float open_logit(float v) { return fmaxf(v, -INFINITY); }
+// e^x for x <= 0, a logit's distance from the largest: 2^(x log2 e) on the special function unit, off by
+// 2 ulp and |x| 2^-23 (what rounding the distance to fp32 costs anyway, twice); 0 below 2^-126.
+__device__ __forceinline__ float exp_below(float x) { return ex2_mufu(x * 1.4426950408889634f); }
 
 // L lanes a token (32 / L tokens a warp), V logits a lane (expert v * L + lane): with eight logits a lane a
 // round of the top-k is a few compares and log2 L shuffles for several tokens at once, where a whole
-// warp a token spends two warp reductions on each. Each round takes the largest key left and the lowest
-// expert that has it.
+// warp a token spends two warp reductions on each. Each round takes the largest logit left and the lowest
+// expert that has it. Bound by instructions (39200 tokens of 64 experts, four each: ROUTETIME us).
 template <int L>
-__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const uint32_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = v > w ? v : w;
-  }
+  for (int o = L / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 template <int L>
 __device__ __forceinline__ int group_min(int v) {
 #pragma unroll
-  for (int o = L / 2; o > 0; o >>= 1) {
-    const int w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = v < w ? v : w;
-  }
+  for (int o = L / 2; o > 0; o >>= 1) v = min(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 template <int L>
@@ -53,10 +42,10 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 template <int V>
-__device__ __forceinline__ uint32_t largest(const uint32_t (&key)[V]) {
-  uint32_t best = key[0];
+__device__ __forceinline__ float largest(const float (&x)[V]) {
+  float best = x[0];
 #pragma unroll
-  for (int v = 1; v < V; ++v) best = best > key[v] ? best : key[v];
+  for (int v = 1; v < V; ++v) best = fmaxf(best, x[v]);
   return best;
 }
 
@@ -71,34 +60,30 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   const int l = threadIdx.x % L;
   const int t = (blockIdx.x * (kRouteWarps * 32) + threadIdx.x) / L;
   const bool live = t < T;
-  uint32_t key[V];
+  float x[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = v * L + l;
-    key[v] = live && e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
+    x[v] = live && e < E ? open_logit(__ldg(logits + (size_t)t * E + e)) : -INFINITY;
   }
-  float top = 0.f, total = 0.f, mine = 0.f;
+  float best = group_max<L>(largest(x));
+  const float top = best > -INFINITY ? best : 0.f;
+  float total = 0.f, mine = 0.f;
   int my_id = -1;
+  if (!renorm) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) total += exp_below(x[v] - top);   // (closed: 2^-inf = 0)
+    total = group_sum<L>(total);
+  }
   for (int j = 0; j < topk; ++j) {
-    const uint32_t best = group_max<L>(largest(key));
+    if (j > 0) best = group_max<L>(largest(x));
+    const bool open = best > -INFINITY;   // else every expert left is closed
     int at = 1 << 30;
 #pragma unroll
     for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) at = v * L + l;
+      if (x[v] == best) at = v * L + l;
     at = group_min<L>(at);
-    const float value = key_value(best);
-    if (j == 0) {
-      top = value;
-      if (!renorm) {
-        float s = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (key[v]) s += expf(key_value(key[v]) - top);
-        total = group_sum<L>(s);
-      }
-    }
-    const bool open = best != 0u;   // else every expert left is closed
-    const float ex = open ? expf(value - top) : 0.f;
+    const float ex = open ? exp_below(best - top) : 0.f;
     if (renorm) total += ex;
     if (l == j && open) {
       mine = ex;
@@ -106,7 +91,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (v * L + l == at) key[v] = 0u;
+      if (v * L + l == at) x[v] = -INFINITY;
   }
   if (live && l < topk) {
     ids[(size_t)t * topk + l] = my_id;
@@ -146,23 +131,22 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   for (int v = 0; v < V; ++v) d[v] = 0.f;
   const float mean = group_sum<L>(w * dw);
   if (!renorm) {
-    uint32_t key[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = v * L + l;
-      key[v] = live && e < E ? rank_key(__ldg(logits + (size_t)t * E + e)) : 0u;
+      d[v] = live && e < E ? open_logit(__ldg(logits + (size_t)t * E + e)) : -INFINITY;
     }
-    const uint32_t best = group_max<L>(largest(key));
-    const float top = key_value(best);
-    float s = 0.f;
+    const float best = group_max<L>(largest(d)), top = best > -INFINITY ? best : 0.f;
+    float total = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (key[v]) d[v] = expf(key_value(key[v]) - top);
-      s += d[v];
+      d[v] = exp_below(d[v] - top);
+      total += d[v];
     }
-    const float total = group_sum<L>(s);
+    total = group_sum<L>(total);
+    const float k = total > 0.f ? -mean / total : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) d[v] = key[v] ? -mean * (d[v] / total) : 0.f;
+    for (int v = 0; v < V; ++v) d[v] *= k;
   }
   const float add = renorm ? w * (dw - mean) : w * dw;
   for (int j = 0; j < topk; ++j) {
@@ -230,26 +214,37 @@ cudaError_t launch_expert_route_backward(const float* logits, const int32_t* ids
 constexpr int kSortWarps = 16;
 constexpr int kSortThreads = kSortWarps * 32;
 
-// Expert of assignment a, or -1 (routed nowhere; an id outside [-1, E) is recorded and dropped).
-__device__ __forceinline__ int sort_expert(const int32_t* ids, int a, int E, int* status) {
-  const int e = __ldg(ids + a);
-  if (e < -1 || e >= E) {
-    record_bad_index(status);
-    return -1;
+// Calls f(a, expert) for every 32 assignments of [a0, a1) in order, by this warp (lane's assignment a, -1 past
+// the end), the ids of four steps loaded together.
+template <class F>
+__device__ __forceinline__ void sort_walk(const int32_t* ids, int a0, int a1, int E, int* status,
+                                          F&& f) {
+  const int lane = threadIdx.x & 31;
+  for (int a = a0 + lane; a - lane < a1; a += 128) {
+    int e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e[i] = a + 32 * i < a1 ? __ldg(ids + a + 32 * i) : -1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (a - lane + 32 * i >= a1) break;
+      if (e[i] < -1 || e[i] >= E) {   // routed nowhere, and recorded
+        record_bad_index(status);
+        e[i] = -1;
+      }
+      f(a + 32 * i, e[i]);
+    }
   }
-  return e;
 }
 
 // counts[e] += the experts of [a0, a1), by this warp.
 __device__ __forceinline__ void sort_count(const int32_t* ids, int a0, int a1, int E, int* counts,
                                            int* status) {
   const int lane = threadIdx.x & 31;
-  for (int a = a0; a < a1; a += 32) {
-    const int e = a + lane < a1 ? sort_expert(ids, a + lane, E, status) : -1;
+  sort_walk(ids, a0, a1, E, status, [&](int, int e) {
     const uint32_t same = __match_any_sync(0xffffffffu, e);
     if (e >= 0 && (same & ((1u << lane) - 1)) == 0) counts[e] += __popc(same);
     __syncwarp();
-  }
+  });
 }
 
 __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int32_t* __restrict__ ids,
@@ -353,34 +348,36 @@ __global__ void __launch_bounds__(kSortThreads)
   }
   __syncthreads();
   int* next = counts + warp * E;
-  for (int a = a0; a < a1; a += 32) {
-    const bool live = a + lane < a1;
-    const int ex = live ? sort_expert(ids, a + lane, E, status) : -1;
+  sort_walk(ids, a0, a1, E, status, [&](int a, int ex) {
     const uint32_t same = __match_any_sync(0xffffffffu, ex);
     const uint32_t lower = same & ((1u << lane) - 1);
     const int at = ex >= 0 ? next[ex] + __popc(lower) : -1;
     __syncwarp();
     if (ex >= 0 && lower == 0) next[ex] += __popc(same);
     __syncwarp();
-    if (live) {
-      if (slot) slot[a + lane] = at;
-      if (order && at >= 0) order[at] = a + lane;
+    if (a < a1) {
+      if (slot) slot[a] = at;
+      if (order && at >= 0) order[at] = a;
       // places past the routed assignments hold none
-      if (order && a + lane >= s_total) order[a + lane] = -1;
+      if (order && a >= s_total) order[a] = -1;
     }
-  }
+  });
 }
 
-// CTAs the sort takes: one up to kSortOne assignments, else one per kSortOne / 8 up to kSortMaxCtas.
+// The sort's CTAs and the assignments of each, a whole number of steps of all its warps: one CTA up to
+// kSortOne assignments (a second launch costs more than the steps), else as few steps as kSortMaxCtas allow.
+static int sort_chunk(long long n) {
+  if (n <= kSortOne) return (int)n;
+  const long long step = kSortThreads;
+  return (int)((n + step * kSortMaxCtas - 1) / (step * kSortMaxCtas) * step);
+}
 int sort_ctas(long long n) {
-  if (n <= kSortOne) return 1;
-  const long long c = (n + kSortOne / 8 - 1) / (kSortOne / 8);
-  return (int)(c < kSortMaxCtas ? c : kSortMaxCtas);
+  return n <= kSortOne ? 1 : (int)((n + sort_chunk(n) - 1) / sort_chunk(n));
 }
 
 cudaError_t launch_expert_count(const int32_t* ids, int32_t* hist, int n, int E, int* status,
                                 cudaStream_t st) {
-  const int ctas = sort_ctas(n), chunk = (n + ctas - 1) / ctas;
+  const int ctas = sort_ctas(n), chunk = sort_chunk(n);
   return launch_pdl(k_expert_count, dim3(ctas), dim3(kSortThreads),
                     (size_t)kSortWarps * E * sizeof(int), st, ids, hist, n, chunk, E, status);
 }
@@ -388,7 +385,7 @@ cudaError_t launch_expert_count(const int32_t* ids, int32_t* hist, int n, int E,
 cudaError_t launch_expert_place(const int32_t* ids, const int32_t* hist, int32_t* order,
                                 int32_t* slot, int32_t* offsets, int n, int E, int* status,
                                 cudaStream_t st) {
-  const int ctas = sort_ctas(n), chunk = n > 0 ? (n + ctas - 1) / ctas : 0;
+  const int ctas = sort_ctas(n), chunk = sort_chunk(n);
   return launch_pdl(k_expert_place, dim3(ctas), dim3(kSortThreads),
                     (size_t)kSortWarps * E * sizeof(int), st, ids, hist, order, slot, offsets, n,
                     chunk, E, status);

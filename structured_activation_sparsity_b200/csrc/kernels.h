@@ -13,6 +13,10 @@ namespace ss {
 constexpr int kRowCtas = 148;           // CTAs the persistent row kernels are planned for (B200's SMs)
 constexpr int kMaxRankTokens = 16384;   // tokens per unit the rank kernel holds in shared memory
 
+// Allows `kernel` `bytes` of dynamic shared memory on the current device (asked of the driver once per
+// kernel, device and size).
+cudaError_t allow_smem(const void* kernel, int bytes);
+
 // The bounded-wait limit of each source file's kernels (see c_wait_limit_ns), current device.
 cudaError_t set_wait_limit_attn(uint64_t ns);
 cudaError_t set_wait_limit_mlp(uint64_t ns);

@@ -404,7 +404,7 @@ static cudaError_t launch_fwd(const NormParams& p, int wpr, int* status, cudaStr
   const size_t smem = (size_t)2 * kFwdWarps * V * 32 * 8 * sizeof(typename T::Store) +
                       (size_t)4 * p.C * sizeof(float);
   const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      allow_smem(reinterpret_cast<const void*>(kernel), (int)smem);
   if (e != cudaSuccess) return e;
   const int per_cta = kFwdWarps / wpr * (32 / LPR);
   const long long ctas = (p.rows + per_cta - 1) / per_cta;
@@ -914,8 +914,7 @@ static cudaError_t launch_bwd(const NormBwdParams& p, const NormShape& g, int* s
   const size_t sums = (size_t)g.rl * 4 * p.C * sizeof(float);
   if (sums > smem) smem = sums;
   const auto kernel = k_norm_residual_backward<T, R, PRE, POST>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kNormRingBytes + 2 * kMaxNormC * (int)sizeof(float));
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kNormRingBytes + 2 * kMaxNormC * (int)sizeof(float));
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(norm_ctas(g)), dim3(kNormThreads), smem, st, p, g, status);
 }
