@@ -65,11 +65,14 @@ __device__ __forceinline__ void f8_get(F8& f, const float* from, int C, int c) {
   f.p[2] = b.x;
   f.p[3] = b.y;
 }
+__device__ __forceinline__ float f2_sum(uint64_t p) {
+  float a, b;
+  f2_unpack(p, a, b);
+  return a + b;
+}
 // The four pairs' sum.
 __device__ __forceinline__ float f8_sum(const F8& f) {
-  float a, b;
-  f2_unpack(f2_add(f2_add(f.p[0], f.p[1]), f2_add(f.p[2], f.p[3])), a, b);
-  return a + b;
+  return f2_sum(f2_add(f2_add(f.p[0], f.p[1]), f2_add(f.p[2], f.p[3])));
 }
 
 // ---- forward --------------------------------------------------------------------------------
@@ -372,28 +375,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
 
 // ---- shared by the persistent backward ------------------------------------------------------
 constexpr int kNormThreads = 512;
-constexpr int kNormRingBytes = 184 * 1024;
+constexpr int kNormSmem = 225 * 1024;
 constexpr int kNormMaxStages = 4;
 
 struct NormShape {
-  long long rows_per_worker;
   int workers, wpg, rl;     // workers in all; warps per worker; workers per CTA
   int stages, stage_bytes;  // ring of one worker
 };
 
-// The workers' geometry for `tensors` rows of C channels a stage and R rows at a time, plus `extra` bytes a row.
-static NormShape norm_shape(long long rows, int C, int es, int tensors, int R, int extra) {
+// Worker w's first row of `rows` shared evenly by `workers`, and the worker of row r.
+__host__ __device__ inline long long first_row(long long rows, int workers, int w) {
+  return rows * w / workers;
+}
+__host__ __device__ inline long long worker_of(long long rows, int workers, long long r) {
+  return ((r + 1) * workers - 1) / rows;
+}
+
+// The workers' geometry for `tensors` rows of C channels and R rows at a time: as many workers a CTA as have
+// two stages each.
+static NormShape norm_shape(long long rows, int C, int es, int tensors, int R) {
   NormShape g;
   g.wpg = (C / 8 + 31) / 32;
-  g.rl = (kNormThreads / 32) / g.wpg;
-  g.stage_bytes = R * (tensors * C * es + extra);
-  while (g.rl > 1 && kNormRingBytes / (g.rl * g.stage_bytes) < 2) --g.rl;
-  g.stages = kNormRingBytes / (g.rl * g.stage_bytes);
+  g.stage_bytes = R * (tensors * C * es + 16);
+  const int kept = 4 * C * (int)sizeof(float);   // what a worker keeps besides its ring
+  g.rl = kNormThreads / 32 / g.wpg;
+  while (g.rl > 1 && g.rl * (2 * g.stage_bytes + kept) > kNormSmem) --g.rl;
+  g.stages = (kNormSmem / g.rl - kept) / g.stage_bytes;
   if (g.stages > kNormMaxStages) g.stages = kNormMaxStages;
   const long long most = (long long)kNormMaxCtas * g.rl;
-  g.rows_per_worker = (rows + most - 1) / most;
-  if (g.rows_per_worker < 1) g.rows_per_worker = 1;
-  g.workers = (int)((rows + g.rows_per_worker - 1) / g.rows_per_worker);
+  g.workers = (int)(rows < most ? rows : most);
   return g;
 }
 
@@ -458,13 +468,13 @@ cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cu
 // Several workers share a CTA (one per SM); at the end their column sums are added in worker order
 // and written as one partial per CTA, which k_norm_reduce adds in CTA order: no atomics, the same
 // result every run.
-template <class T, int R, bool PRE, bool POST>
+template <class T, int R, bool PRE, bool POST, bool FULL>
 __global__ void __launch_bounds__(kNormThreads, 1)
     k_norm_residual_backward(const NormBwdParams p, const NormShape g, int* status) {
   using S = typename T::Store;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[16 * kNormMaxStages];
-  __shared__ float2 red[2][16][R];   // [buffer][warp][row]
+  __shared__ __align__(8) float red[2][16 * 2 * R];   // [buffer][warp][row][sum]
   __shared__ int abort_flag;
   constexpr int kTensors = PRE ? 4 : 2;
   constexpr bool kStats = PRE || POST;
@@ -472,7 +482,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   const int rl = warp / g.wpg, wg = warp % g.wpg;
   const int tw = wg * 32 + lane, c = tw * 8;
   const int worker = blockIdx.x * g.rl + rl;
-  const bool col = c < p.C && rl < g.rl;
+  const bool col = (FULL || c < p.C) && rl < g.rl;
   if (threadIdx.x == 0) {
     for (int i = 0; i < g.rl * g.stages; ++i) mbar_init(full + i, 1);
     abort_flag = 0;
@@ -482,13 +492,15 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   griddep_wait();
   griddep_launch();
 
-  const long long r0 = (long long)worker * g.rows_per_worker;
-  long long r1 = r0 + g.rows_per_worker;
-  if (r1 > p.rows) r1 = p.rows;
+  const long long r0 = worker < g.workers ? first_row(p.rows, g.workers, worker) : p.rows;
+  const long long r1 = worker < g.workers ? first_row(p.rows, g.workers, worker + 1) : p.rows;
   uint8_t* ring = smem + (size_t)rl * g.stages * g.stage_bytes;
-  // P1 and P0 of the worker's closed groups (with a gate): [2][C] behind the rings.
-  float* closed = reinterpret_cast<float*>(smem + (size_t)g.rl * g.stages * g.stage_bytes) +
-                  (size_t)rl * 2 * p.C + c;
+  // Behind the rings, of each worker: pre_w, coef = gate * scale * post_w (as f8_put lays them out: two
+  // vectors read once a step cost less than the 16 registers, which spilled), and P1 and P0 of its
+  // closed groups (with a gate).
+  float* kept = reinterpret_cast<float*>(smem + (size_t)g.rl * g.stages * g.stage_bytes) +
+                (size_t)rl * 4 * p.C;
+  float* closed = kept + 2 * p.C + c;
   uint64_t* bar = full + rl * g.stages;
   const int row_bytes = p.C * (int)sizeof(S);
   const bool dense = p.ld_x == p.C && p.ld_y == p.C && p.ld_n == p.C;
@@ -520,16 +532,13 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   if (rl < g.rl && tw == 0)
     for (int s = 0; s < g.stages && ahead < r1; ++s, ahead += R) fetch(ahead, s);
 
-  F8 w_pre, coef;                       // coef = gate * scale * post_w
   F8 acc_pw, acc_pb, acc_a, acc_b;
-  f8_fill(w_pre, 0.f);
-  f8_fill(coef, 0.f);
   f8_fill(acc_pw, 0.f);
   f8_fill(acc_pb, 0.f);
   f8_fill(acc_a, 0.f);
   f8_fill(acc_b, 0.f);
   auto load_coef = [&](long long group) {
-    F8 f;
+    F8 coef, f;
     load_f8<T>(coef, p.post_w, c, 1.f);
     load_f8<T>(f, p.scale, c, 1.f);
 #pragma unroll
@@ -539,9 +548,14 @@ __global__ void __launch_bounds__(kNormThreads, 1)
 #pragma unroll
       for (int q = 0; q < 4; ++q) coef.p[q] = f2_mul(coef.p[q], f.p[q]);
     }
+    f8_put(kept + p.C, p.C, c, coef);
   };
   if (col) {
-    if (PRE) load_f8<T>(w_pre, p.pre_w, c, 1.f);
+    if (PRE) {
+      F8 w;
+      load_f8<T>(w, p.pre_w, c, 1.f);
+      f8_put(kept, p.C, c, w);
+    }
     if (!p.gate) load_coef(0);
     if (p.gate) {
 #pragma unroll
@@ -552,14 +566,15 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     if (g.wpg > 1) named_barrier(1 + rl, g.wpg * 32);
     else __syncwarp();
   };
-  // (a, b) of each row summed over the worker's threads: after the first exchange the two halves of a
-  // warp carry one sum each (two rows: after the second, the quarters), so that R rows cost five or
-  // six shuffles.
+  // (a, b) of each of N rows summed over the worker's threads: after the first exchange the two halves of a
+  // warp carry one sum each (two rows: after the second, the quarters), so that N rows cost five or six
+  // shuffles. The warps' sums meet in shared memory as [warp][row][sum] and are added in warp order.
   int buf = 0;
-  auto worker_sums = [&](float (&a)[R], float (&b)[R], auto&& met) {
+  auto worker_sums = [&](auto& a, auto& b, auto&& met) {
+    constexpr int N = sizeof(a) / sizeof(float);
     const bool hi = lane & 16;
     float v;
-    if constexpr (R == 1) {
+    if constexpr (N == 1) {
       v = hi ? b[0] : a[0];
       v += __shfl_xor_sync(0xffffffffu, hi ? a[0] : b[0], 16);
 #pragma unroll
@@ -576,25 +591,25 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
     // lane 16 h + 8 i holds row i's sum h
     if (g.wpg > 1) {
-      float* mine = reinterpret_cast<float*>(&red[buf][warp][0]);
-      if ((lane & (R == 1 ? 15 : 7)) == 0) mine[R == 1 ? lane >> 4 : ((lane >> 2) & 2) + (lane >> 4)] = v;
+      float* all = &red[buf][(warp - wg) * 2 * R];
+      if ((lane & (N == 1 ? 15 : 7)) == 0)
+        all[wg * 2 * N + (N == 1 ? lane >> 4 : ((lane >> 2) & 2) + (lane >> 4))] = v;
       met();
 #pragma unroll
-      for (int i = 0; i < R; ++i) a[i] = b[i] = 0.f;
+      for (int i = 0; i < N; ++i) a[i] = b[i] = 0.f;
 #pragma unroll 4
-      for (int w = 0; w < g.wpg; ++w) {
+      for (int w = 0; w < g.wpg; ++w)
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-          const float2 e = red[buf][warp - wg + w][i];
+        for (int i = 0; i < N; ++i) {
+          const float2 e = reinterpret_cast<const float2*>(all)[w * N + i];
           a[i] += e.x;
           b[i] += e.y;
         }
-      }
       buf ^= 1;
     } else {
       met();
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
+      for (int i = 0; i < N; ++i) {
         a[i] = __shfl_sync(0xffffffffu, v, 8 * i);
         b[i] = __shfl_sync(0xffffffffu, v, 16 + 8 * i);
       }
@@ -647,19 +662,16 @@ __global__ void __launch_bounds__(kNormThreads, 1)
   };
   S* dx = static_cast<S*>(p.dx) + r0 * p.ld_x + c;
   S* dy = static_cast<S*>(p.dy) + r0 * p.ld_y + c;
-  // One step: rows r .. r + n - 1 (n <= R), at rows `at`.. of stage st; `last`: nothing of the stage is
-  // needed after it.
-  auto step = [&](int n, int at, int st, bool last) {
+  // One step: N rows (N <= R), rows `at`.. of stage st; `last`: nothing of the stage is needed after it.
+  auto step = [&](auto rows_n, int at, int st, bool last) {
+    constexpr int N = decltype(rows_n)::value;
     const uint8_t* sp = ring + (size_t)st * g.stage_bytes;
     const float4* stat = reinterpret_cast<const float4*>(sp) + at;
     const S* rows = reinterpret_cast<const S*>(sp + R * 16) + at * p.C + c;
     const int next = R * p.C;   // from one input's rows to the next's
-    bool live[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) live[i] = col && (R == 1 || i < n);
     auto read = [&](F8& f, int which, int i) {
       Chunk<T> t;
-      if (live[i]) chunk_load(t, rows + which * next + i * p.C);
+      if (FULL || col) chunk_load(t, rows + which * next + i * p.C);
       else chunk_zero(t);
       f8_unpack(t, f);
     };
@@ -671,35 +683,35 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         ahead += R;
       }
     };
-    F8 D[R], h[R];
-    float a[R], b[R];
+    F8 D[N], h[N];
+    float a[N], b[N];
     if constexpr (PRE) {
-      F8 dn[R];
+      F8 dn[N], w_pre;
+      if (FULL || col) f8_get(w_pre, kept, p.C, c);
+      else f8_fill(w_pre, 0.f);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
+      for (int i = 0; i < N; ++i) {
         read(h[i], 2, i);
         read(dn[i], 3, i);
-        // (an absent row's statistics are whatever the stage held: not to be multiplied by 0)
-        const float2 t = R == 1 || i < n ? reinterpret_cast<const float2*>(stat + i)[1]
-                                         : make_float2(0.f, 0.f);
+        const float2 t = reinterpret_cast<const float2*>(stat + i)[1];
         const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
-        F8 s1;
+        uint64_t s1 = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
           acc_pw.p[q] = f2_fma(dn[i].p[q], h[i].p[q], acc_pw.p[q]);
           acc_pb.p[q] = f2_add(acc_pb.p[q], dn[i].p[q]);
           dn[i].p[q] = f2_mul(dn[i].p[q], w_pre.p[q]);
-          s1.p[q] = f2_mul(dn[i].p[q], h[i].p[q]);
+          s1 = f2_fma(dn[i].p[q], h[i].p[q], s1);
         }
         a[i] = f8_sum(dn[i]);
-        b[i] = f8_sum(s1);
+        b[i] = f2_sum(s1);
       }
       worker_sums(a, b, meet);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
+      for (int i = 0; i < N; ++i) {
         read(D[i], 0, i);
-        const float r = R == 1 || i < n ? stat[i].w : 0.f;
+        const float r = stat[i].w;
         const uint64_t rs = f2_same(r);
         const uint64_t k0 = f2_same(-r * (a[i] * mean_on)), k1 = f2_same(-r * (b[i] * inv_c));
 #pragma unroll
@@ -708,16 +720,18 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < R; ++i) read(D[i], 0, i);
+      for (int i = 0; i < N; ++i) read(D[i], 0, i);
     }
+    F8 coef;
+    if (FULL || col) f8_get(coef, kept + p.C, p.C, c);
+    else f8_fill(coef, 0.f);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
+    for (int i = 0; i < N; ++i) {
       // h_post (or y), the column sums and, with a post norm, the row sums.
       read(h[i], 1, i);
-      if (live[i]) f8_store<T>(dx + i * p.ld_x, D[i]);
+      if (FULL || col) f8_store<T>(dx + i * p.ld_x, D[i]);
       if constexpr (POST) {
-        const float2 t = R == 1 || i < n ? *reinterpret_cast<const float2*>(stat + i)
-                                         : make_float2(0.f, 0.f);
+        const float2 t = *reinterpret_cast<const float2*>(stat + i);
         const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
@@ -729,20 +743,20 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         D[i].p[q] = f2_mul(D[i].p[q], coef.p[q]);
       }
       if constexpr (POST) {
-        F8 s1;
+        uint64_t s1 = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s1.p[q] = f2_mul(D[i].p[q], h[i].p[q]);
+        for (int q = 0; q < 4; ++q) s1 = f2_fma(D[i].p[q], h[i].p[q], s1);
         a[i] = f8_sum(D[i]);
-        b[i] = f8_sum(s1);
+        b[i] = f2_sum(s1);
       }
     }
     if constexpr (POST) {
-      float rstd[R];
+      float rstd[N];
 #pragma unroll
-      for (int i = 0; i < R; ++i) rstd[i] = R == 1 || i < n ? stat[i].y : 0.f;
+      for (int i = 0; i < N; ++i) rstd[i] = stat[i].y;
       worker_sums(a, b, release);
 #pragma unroll
-      for (int i = 0; i < R; ++i) {
+      for (int i = 0; i < N; ++i) {
         const uint64_t rs = f2_same(rstd[i]);
         const uint64_t k0 = f2_same(-rstd[i] * (a[i] * mean_on));
         const uint64_t k1 = f2_same(-rstd[i] * (b[i] * inv_c));
@@ -753,10 +767,10 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
     if constexpr (!POST) release();
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      if (live[i]) f8_store<T>(dy + i * p.ld_y, D[i]);
-    dx += n * p.ld_x;
-    dy += n * p.ld_y;
+    for (int i = 0; i < N; ++i)
+      if (FULL || col) f8_store<T>(dy + i * p.ld_y, D[i]);
+    dx += N * p.ld_x;
+    dy += N * p.ld_y;
   };
   if (rl < g.rl) {
     int st = 0, phase = 0;
@@ -775,9 +789,13 @@ __global__ void __launch_bounds__(kNormThreads, 1)
           group_end = (group + 1) * p.rows_per_gate;
           if (col) load_coef(group);
         }
-        const int m = (int)(group_end - at < n - done ? group_end - at : n - done);
-        step(m, done, st, done + m == n);
-        done += m;
+        if (R == 2 && done == 0 && n == 2 && group_end - at >= 2) {
+          step(std::integral_constant<int, R>{}, 0, st, true);
+          done = 2;
+        } else {
+          step(std::integral_constant<int, 1>{}, done, st, done + 1 == n);
+          ++done;
+        }
       } while (done < n);
       if (++st == g.stages) {
         st = 0;
@@ -786,8 +804,8 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
     if (p.gate) close_group();
   }
-  // The CTA's column sums, in worker order: [pre_w, pre_b, P1, P0][C]. The rings are free now: every
-  // copy into them has been waited for (the closed groups' sums are read before they are overwritten).
+  // The CTA's column sums, in worker order: [pre_w, pre_b, P1, P0][C], over what the workers kept (the closed
+  // groups' sums are read before they are overwritten).
   F8 p1 = acc_a, p0 = acc_b;
   if (p.gate && col) {
 #pragma unroll
@@ -797,7 +815,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
   }
   __syncthreads();
-  float* sums = reinterpret_cast<float*>(smem);
+  float* sums = kept - (size_t)rl * 4 * p.C;
   if (col) {
     float* mine = sums + (size_t)rl * 4 * p.C + c;
 #pragma unroll
@@ -868,13 +886,14 @@ __global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, cons
     const long long g0 = gr * p.rows_per_gate;
     long long g1 = g0 + p.rows_per_gate;
     if (g1 > p.rows) g1 = p.rows;
-    const long long w0 = g0 / g.rows_per_worker, w1 = (g1 - 1) / g.rows_per_worker;
+    const long long w0 = worker_of(p.rows, g.workers, g0);
+    const long long w1 = worker_of(p.rows, g.workers, g1 - 1);
     if (w0 == w1) continue;   // one worker's: written by it
     float s = 0.f;
     if (c < p.C)
 #pragma unroll 4
       for (long long w = w0 + warp; w <= w1; w += 16)
-        s += p.gate_partial[(w * 2 + (g0 > w * g.rows_per_worker ? 1 : 0)) * p.C + c];
+        s += p.gate_partial[(w * 2 + (g0 > first_row(p.rows, g.workers, (int)w) ? 1 : 0)) * p.C + c];
     part[0][warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < p.C) {
@@ -886,13 +905,13 @@ __global__ void __launch_bounds__(512) k_norm_reduce(const NormBwdParams p, cons
   }
 }
 
-// Two rows a step, or one where two would not leave two stages.
+// Two rows a step, or one where two rows' stages would cost more than a third of the workers.
 static NormShape bwd_shape(long long rows, int C, int es, bool pre, int* R) {
   *R = 2;
-  NormShape g = norm_shape(rows, C, es, pre ? 4 : 2, 2, 16);
-  if (g.stages < 2 || g.rl < (kNormThreads / 32) / g.wpg) {
+  NormShape g = norm_shape(rows, C, es, pre ? 4 : 2, 2);
+  if (g.stages < 2 || 3 * g.rl < 2 * (kNormThreads / 32 / g.wpg)) {
     *R = 1;
-    g = norm_shape(rows, C, es, pre ? 4 : 2, 1, 16);
+    g = norm_shape(rows, C, es, pre ? 4 : 2, 1);
   }
   return g;
 }
@@ -909,12 +928,12 @@ size_t norm_backward_partial(long long rows, int C, int es, bool pre, bool gate,
 template <class T, int R, bool PRE, bool POST>
 static cudaError_t launch_bwd(const NormBwdParams& p, const NormShape& g, int* status,
                               cudaStream_t st) {
-  size_t smem = (size_t)g.rl * g.stages * g.stage_bytes +
-                (p.gate ? (size_t)g.rl * 2 * p.C * sizeof(float) : 0);
-  const size_t sums = (size_t)g.rl * 4 * p.C * sizeof(float);
-  if (sums > smem) smem = sums;
-  const auto kernel = k_norm_residual_backward<T, R, PRE, POST>;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kNormRingBytes + 2 * kMaxNormC * (int)sizeof(float));
+  const size_t smem = (size_t)g.rl * g.stages * g.stage_bytes +
+                      (size_t)g.rl * 4 * p.C * sizeof(float);
+  const auto kernel = p.C % 256 == 0 ? k_norm_residual_backward<T, R, PRE, POST, true>
+                                     : k_norm_residual_backward<T, R, PRE, POST, false>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel),
+                                   kNormSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3(norm_ctas(g)), dim3(kNormThreads), smem, st, p, g, status);
 }
