@@ -363,12 +363,14 @@ int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int3
                                cfg->topk, E, C, H, status, st);
     }));
   }
-  CUtensorMap tw1, tx, tw2, th;
+  CUtensorMap tw1, tx, tx_half, tw2, th, th_half;
   const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!encode_bf16(&tw1, 2, w1, C, (uint64_t)E * H, 1, (uint64_t)C * 2, 64, 128, sw) ||
-      !encode_bf16(&tx, 2, xs, C, n, 1, (uint64_t)C * 2, 64, expert_box(L.fc1.tn), sw) ||
+      !encode_bf16(&tx, 2, xs, C, n, 1, (uint64_t)C * 2, 64, L.fc1.box, sw) ||
+      !encode_bf16(&tx_half, 2, xs, C, n, 1, (uint64_t)C * 2, 64, L.fc1.box / 2, sw) ||
       !encode_bf16(&tw2, 2, w2, H, (uint64_t)E * C, 1, (uint64_t)H * 2, 64, 128, sw) ||
-      !encode_bf16(&th, 2, h, H, n, 1, (uint64_t)H * 2, 64, expert_box(L.fc2.tn), sw))
+      !encode_bf16(&th, 2, h, H, n, 1, (uint64_t)H * 2, 64, L.fc2.box, sw) ||
+      !encode_bf16(&th_half, 2, h, H, n, 1, (uint64_t)H * 2, 64, L.fc2.box / 2, sw))
     return SS_ECUDA;
   if ((rc = sort_launch(ids, nullptr, slot, offsets, n, E, wsb + L.sort, status, st))) return rc;
   rc = cuda_err(traced("expert_gather", st, [&] {
@@ -388,7 +390,7 @@ int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int3
   g.kb_total = (C + 63) / 64;
   g.gelu = 1;
   rc = cuda_err(traced("expert_fc1", st, [&] {
-    return launch_expert_gemm(&tw1, &tx, L.fc1, g, sm_count(), status, st);
+    return launch_expert_gemm(&tw1, &tx, &tx_half, L.fc1, g, sm_count(), status, st);
   }));
   if (rc) return rc;
   const int splits = L.fc2.splits;
@@ -401,7 +403,7 @@ int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int3
   g.kb_total = (H + 63) / 64;
   g.gelu = 0;
   rc = cuda_err(traced("expert_fc2", st, [&] {
-    return launch_expert_gemm(&tw2, &th, L.fc2, g, sm_count(), status, st);
+    return launch_expert_gemm(&tw2, &th, &th_half, L.fc2, g, sm_count(), status, st);
   }));
   if (rc) return rc;
   return cuda_err(traced("expert_combine", st, [&] {

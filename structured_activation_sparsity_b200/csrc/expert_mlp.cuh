@@ -29,13 +29,15 @@ static_assert(128 * kXRegsProducer + 256 * kXRegsEpilogue <= 384 * 168,
 // in 2 KB of shared memory: 64 bytes a row, so that it stores 16 bytes a lane, eight rows an instruction.
 constexpr int kXTurn = 32 * 64;
 
-// Token tile TN: a stage holds one 64-wide k-block of 128 weight rows and up to TN token rows, which come
-// in boxes of kBox rows, as many as the tile has rows for.
-template <int TN>
+// Token tile TN: a stage holds one 64-wide k-block of 128 weight rows and up to TN token rows. These come in
+// one box, of all the tile's rows or of half of them if that holds what the tile has: the issue of a load
+// costs its thread over a hundred cycles, and with a box per 32 rows the tensor cores waited for that
+// half of the time. PAIR: two CTAs work on a tile of 256 weight rows, each with 128 of them and half of
+// the token rows.
+template <int TN, bool PAIR>
 struct XCfg {
-  static constexpr int kBox = expert_box(TN);
-  static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = TN * 128;
+  static constexpr int kBox = expert_box(TN, PAIR);   // rows of the larger box
+  static constexpr int kABytes = 128 * 128;  static constexpr int kBBytes = kBox * 128;
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kStages = (192 * 1024) / kStageBytes < 10 ? (192 * 1024) / kStageBytes : 10;
   static constexpr int kBar = kStages * kStageBytes;
@@ -51,11 +53,11 @@ struct XUnit {
   int m0, s, kb0, kb1;   // first feature, k-split and its k-blocks
 };
 
-template <int TN>
+template <int TN, bool PAIR>
 __global__ void __launch_bounds__(kXThreads, 1)
     k_expert_gemm(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
-                  const ExpertGemm g, int* status) {
-  using G = XCfg<TN>;
+                  const __grid_constant__ CUtensorMap tb_half, const ExpertGemm g, int* status) {
+  using G = XCfg<TN, PAIR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -76,12 +78,15 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_full + b, 1);
-      mbar_init(acc_empty + b, kXEpiThreads);
+      mbar_init(acc_empty + b, (PAIR ? 2 : 1) * kXEpiThreads / 32);
     }
     *abort = 0;
     fence_barrier_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, G::kTmemCols);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc_pair(tmem_slot, G::kTmemCols);
+    else tmem_alloc(tmem_slot, G::kTmemCols);
+  }
   griddep_wait();
   griddep_launch();
   // The experts' tiles: warp 2 sums ceil(rows / TN) over the experts, 32 at a time.
@@ -108,17 +113,27 @@ __global__ void __launch_bounds__(kXThreads, 1)
       base += __shfl_sync(0xffffffffu, x, 31);
     }
   }
+  // The whole cluster (PAIR: the barriers that the other CTA arrives on are set up, too).
+  auto meet = [&] {
+    if constexpr (PAIR) cluster_sync_converged();
+    else cta_sync_converged();
+  };
   tc_fence_before();
-  cta_sync_converged();
+  meet();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int units = tile_start[g.E] * g.m_tiles * g.splits;
+  // The pair takes its units together; its first CTA issues the MMAs.
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int first = PAIR ? blockIdx.x / 2 : blockIdx.x, step = PAIR ? gridDim.x / 2 : gridDim.x;
+  // Columns of the tile's MMA: its rows, rounded up to the instruction's step (PAIR: of each half).
+  auto columns = [](int rows) { return PAIR ? (rows + 31) & ~31 : (rows + 15) & ~15; };
 
   auto decode = [&](int u) {
     XUnit r;
     r.s = u % g.splits;
     const int v = u / g.splits;
-    r.m0 = v % g.m_tiles * 128;
+    r.m0 = v % g.m_tiles * (PAIR ? 256 : 128) + rank * 128;
     const int t = v / g.m_tiles;
     int lo = 0, hi = g.E;   // tile_start[lo] <= t < tile_start[hi]
     while (hi - lo > 1) {
@@ -140,53 +155,80 @@ __global__ void __launch_bounds__(kXThreads, 1)
     if (warp == 0 && lane == 0) {
       tma_prefetch_desc(&ta);
       tma_prefetch_desc(&tb);
-      int it = 0;
+      tma_prefetch_desc(&tb_half);
+      // (One thread's instructions between two loads are time the tensor cores may wait: the loop keeps
+      // its stage and phase, and addresses are added up.)
+      const uint32_t bar0 = PAIR ? cluster_addr(full, 0) : smem_u32(full);
+      int st = 0, phase = 1;   // the first round finds every stage free
       bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x) {
+      for (int u = first; ok && u < units; u += step) {
         const XUnit r = decode(u);
-        const int nk = r.kb1 - r.kb0, boxes = (r.rows + G::kBox - 1) / G::kBox;
-        for (int j = 0; j < nk; ++j, ++it) {
-          const int st = it % G::kStages;
-          if (it >= G::kStages &&
-              !(ok = mbar_wait(empty + st, ((it / G::kStages) - 1) & 1, abort, status)))
-            break;
+        // This CTA's token rows (PAIR: its half of the columns).
+        const int mine = PAIR ? columns(r.rows) / 2 : r.rows, row0 = r.row0 + rank * mine;
+        const bool half = mine <= G::kBox / 2;
+        const CUtensorMap* map = half ? &tb_half : &tb;
+        const uint32_t bytes = G::kABytes + (half ? G::kBBytes / 2 : G::kBBytes);
+        const int f = r.e * g.features + r.m0;
+        for (int kc = r.kb0 * 64; kc < r.kb1 * 64; kc += 64) {
+          if (!(ok = mbar_wait(empty + st, phase, abort, status))) break;
           uint8_t* sa = smem + st * G::kStageBytes;
-          mbar_expect_tx(full + st, G::kABytes + boxes * G::kBox * 128);
-          tma_load_2d(sa, &ta, full + st, (r.kb0 + j) * 64, r.e * g.features + r.m0);
-          for (int b = 0; b < boxes; ++b)
-            tma_load_2d(sa + G::kABytes + b * G::kBox * 128, &tb, full + st, (r.kb0 + j) * 64,
-                        r.row0 + b * G::kBox);
+          if constexpr (PAIR) {
+            // Both CTAs' loads count on the first one's barrier, whose MMAs read both.
+            if (rank == 0) mbar_expect_tx(full + st, 2 * bytes);
+            tma_load_2d_pair(sa, &ta, bar0 + st * 8, kc, f);
+            tma_load_2d_pair(sa + G::kABytes, map, bar0 + st * 8, kc, row0);
+          } else {
+            mbar_expect_tx(full + st, bytes);
+            tma_load_2d(sa, &ta, full + st, kc, f);
+            tma_load_2d(sa + G::kABytes, map, full + st, kc, row0);
+          }
+          if (++st == G::kStages) {
+            st = 0;
+            phase ^= 1;
+          }
         }
       }
-    } else if (warp == 1 && lane == 0) {
-      int it = 0, i = 0;
-      bool ok = true;
-      for (int u = blockIdx.x; ok && u < units; u += gridDim.x, ++i) {
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // Descriptors of the first stage; others are added to (addresses count in 16 bytes).
+      const uint64_t desc0 = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128B);
+      int st = 0, phase = 0, i = 0;
+      bool ok = true, ready = mbar_test(full, 0);
+      for (int u = first; ok && u < units; u += step, ++i) {
         const XUnit r = decode(u);
-        const uint32_t idesc = idesc_bf16_f32(128, (r.rows + 15) & ~15, false, false);
+        const uint32_t idesc = idesc_bf16_f32(PAIR ? 256 : 128, columns(r.rows), false, false);
         const int buf = i & 1;
-        if (i >= 2 && !(ok = mbar_wait(acc_empty + buf, ((i >> 1) - 1) & 1, abort, status))) break;
+        if (i >= 2 &&
+            !(ok = PAIR ? mbar_wait_cluster(acc_empty + buf, ((i >> 1) - 1) & 1, abort, status)
+                        : mbar_wait(acc_empty + buf, ((i >> 1) - 1) & 1, abort, status)))
+          break;
         tc_fence_after();
         const uint32_t d = tmem + buf * TN;
-        const int nk = r.kb1 - r.kb0;
-        bool ready = mbar_test(full + it % G::kStages, (it / G::kStages) & 1);
-        for (int j = 0; j < nk; ++j, ++it) {
-          const int st = it % G::kStages;
-          if (!__builtin_expect(ready, 1) &&
-              !(ok = mbar_wait(full + st, (it / G::kStages) & 1, abort, status)))
+        uint32_t more = 0;   // the unit's first MMA clears the accumulator
+        for (int left = r.kb1 - r.kb0; left > 0; --left) {
+          if (!__builtin_expect(ready, 1) && !(ok = mbar_wait(full + st, phase, abort, status)))
             break;
-          if (j + 1 < nk) ready = mbar_test(full + (it + 1) % G::kStages, ((it + 1) / G::kStages) & 1);
+          const int cur = st;
+          if (++st == G::kStages) {
+            st = 0;
+            phase ^= 1;
+          }
+          ready = mbar_test(full + st, phase);   // the next stage's, behind this one's MMAs
           tc_fence_after();
-          const uint32_t a_addr = smem_u32(smem + st * G::kStageBytes);
-          const uint32_t b_addr = a_addr + G::kABytes;
+          const uint64_t a = desc0 + (uint64_t)cur * (G::kStageBytes >> 4);
+          const uint64_t b = a + (G::kABytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            umma_bf16_ss(d, smem_desc(a_addr + kk * 32, 16, 1024, kSwizzle128B),
-                         smem_desc(b_addr + kk * 32, 16, 1024, kSwizzle128B), idesc,
-                         (j > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(empty + st);
+          for (int kk = 0; kk < 4; ++kk) {
+            if constexpr (PAIR) umma_bf16_ss_pair(d, a + 2 * kk, b + 2 * kk, idesc, more);
+            else umma_bf16_ss(d, a + 2 * kk, b + 2 * kk, idesc, more);
+            more = 1;
+          }
+          if constexpr (PAIR) umma_commit_pair(empty + cur);
+          else umma_commit(empty + cur);
         }
-        if (ok) umma_commit(acc_full + buf);
+        if (ok) {
+          if constexpr (PAIR) umma_commit_pair(acc_full + buf);
+          else umma_commit(acc_full + buf);
+        }
       }
     }
   } else {
@@ -197,7 +239,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     const uint32_t lane_off = uint32_t(32 * quad) << 16;
     uint16_t* turn = reinterpret_cast<uint16_t*>(smem + G::kTurn + (warp - 4) * kXTurn);
     int i = 0;
-    for (int u = blockIdx.x; u < units; u += gridDim.x, ++i) {
+    for (int u = first; u < units; u += step, ++i) {
       const XUnit r = decode(u);
       const int buf = i & 1;
       const int f0 = r.m0 + 32 * quad, f = f0 + lane;
@@ -243,25 +285,34 @@ __global__ void __launch_bounds__(kXThreads, 1)
         }
       }
       tc_fence_before();
-      mbar_arrive(acc_empty + buf);
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(acc_empty + buf, 0));
+        else mbar_arrive(acc_empty + buf);
+      }
     }
   }
   tc_fence_before();
-  cta_sync_converged();
+  meet();   // (PAIR: nothing of the other CTA's is in use any more, either)
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, G::kTmemCols);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, G::kTmemCols);
+    else tmem_dealloc(tmem, G::kTmemCols);
   }
 }
 
 ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms) {
   ExpertGemmPlan p;
-  p.m_tiles = (features + 127) / 128;
   // A token tile of twice an average expert's rows: an expert with one row more than the tile reads its
   // weights again for a second one (784 tokens over 16 experts, 98 rows on average: 98 us with tiles of
   // 128, 87 us with 256), while what a tile does not fill is not loaded.
   const long long avg = (n + E - 1) / E;
   p.tn = avg <= 32 ? 64 : avg <= 64 ? 128 : 256;
+  // Pairs of CTAs where tiles are wide.
+  p.pair = p.tn == 256;
+  p.box = expert_box(p.tn, p.pair);
+  const int workers = p.pair ? sms / 2 : sms;
+  p.m_tiles = (features + (p.pair ? 255 : 127)) / (p.pair ? 256 : 128);
   // Tiles at most: one per expert with rows, and one more per full tile.
   long long tiles = n / p.tn + (n < E ? n : E);
   if (tiles > n) tiles = n;
@@ -269,31 +320,32 @@ ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool s
   p.splits = 1;
   const int kb = (Kd + 63) / 64;
   if (split)
-    while (p.splits < 8 && p.max_units * (p.splits + 1) <= sms && kb / (p.splits + 1) >= 4)
+    while (p.splits < 8 && p.max_units * (p.splits + 1) <= workers && kb / (p.splits + 1) >= 4)
       ++p.splits;
   p.max_units *= p.splits;
   return p;
 }
 
-template <int TN>
-static cudaError_t launch_x(const CUtensorMap* ta, const CUtensorMap* tb, const ExpertGemm& g,
-                            int grid, int* status, cudaStream_t st) {
-  using G = XCfg<TN>;
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(k_expert_gemm<TN>), G::kAlloc);
+template <int TN, bool PAIR>
+static cudaError_t launch_x(const CUtensorMap* ta, const CUtensorMap* tb,
+                            const CUtensorMap* tb_half, const ExpertGemmPlan& p,
+                            const ExpertGemm& g, int sms, int* status, cudaStream_t st) {
+  using G = XCfg<TN, PAIR>;
+  const auto kernel = k_expert_gemm<TN, PAIR>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), G::kAlloc);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_expert_gemm<TN>, dim3(grid), dim3(kXThreads), G::kAlloc, st, *ta, *tb, g,
-                    status);
+  const int workers = PAIR ? sms / 2 : sms;
+  const int grid = (int)(p.max_units < workers ? p.max_units : workers) * (PAIR ? 2 : 1);
+  return launch_pdl_clusters(kernel, PAIR ? 2 : 1, dim3(grid), dim3(kXThreads), G::kAlloc, st, *ta,
+                             *tb, *tb_half, g, status);
 }
 
 cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
-                               const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
-                               cudaStream_t st) {
-  const int grid = (int)(p.max_units < sms ? p.max_units : sms);
-  switch (p.tn) {
-    case 64: return launch_x<64>(ta, tb, g, grid, status, st);
-    case 128: return launch_x<128>(ta, tb, g, grid, status, st);
-    default: return launch_x<256>(ta, tb, g, grid, status, st);
-  }
+                               const CUtensorMap* tb_half, const ExpertGemmPlan& p,
+                               const ExpertGemm& g, int sms, int* status, cudaStream_t st) {
+  if (p.tn == 64) return launch_x<64, false>(ta, tb, tb_half, p, g, sms, status, st);
+  if (p.tn == 128) return launch_x<128, false>(ta, tb, tb_half, p, g, sms, status, st);
+  return launch_x<256, true>(ta, tb, tb_half, p, g, sms, status, st);
 }
 
 // ---- few rows -----------------------------------------------------------------------------------

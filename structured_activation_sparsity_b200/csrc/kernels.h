@@ -283,17 +283,19 @@ struct ExpertGemm {
   int E, features, m_tiles, splits, kb_total, gelu;
 };
 struct ExpertGemmPlan {
-  int tn, m_tiles, splits;   // token tile, feature tiles, k-splits
+  int tn, box;               // rows of a token tile, and of a CTA's box of it
+  bool pair;                 // two CTAs a tile of 256 features (else one CTA, 128)
+  int m_tiles, splits;       // feature tiles, k-splits
   long long max_units;       // at most
 };
 ExpertGemmPlan expert_gemm_plan(long long n, int E, int features, int Kd, bool split, int sms);
-// Rows of a token box of a tile of tn rows.
-__host__ __device__ constexpr int expert_box(int tn) { return tn < 256 ? 32 : 64; }
-// ta: weights [E * features, Kd], box 128 rows; tb: rows [n, Kd], box expert_box(p.tn) rows; both 64
-// columns.
+// Rows of a CTA's token box of a tile of tn rows.
+__host__ __device__ constexpr int expert_box(int tn, bool pair) { return pair ? tn / 2 : tn; }
+// ta: weights [E * features, Kd], box 128 rows; tb, tb_half: rows [n, Kd], boxes of p.box rows and of half
+// as many; all 64 columns.
 cudaError_t launch_expert_gemm(const CUtensorMap* ta, const CUtensorMap* tb,
-                               const ExpertGemmPlan& p, const ExpertGemm& g, int sms, int* status,
-                               cudaStream_t st);
+                               const CUtensorMap* tb_half, const ExpertGemmPlan& p,
+                               const ExpertGemm& g, int sms, int* status, cudaStream_t st);
 
 // The products of a few assignments, straight from the unsorted tokens (see expert_mlp.cuh): fc1 (x [tokens,
 // ld], weights [E, rows, K] -> out: the hidden rows [n, rows]) or fc2 (x: the hidden rows [n, K] -> out
