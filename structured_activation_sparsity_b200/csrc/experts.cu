@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   griddep_wait();
   griddep_launch();
   const int l = threadIdx.x % L;
-  const int t = (blockIdx.x * (kRouteWarps * 32) + threadIdx.x) / L;
+  const int t = blockIdx.x * (kRouteWarps * 32 / L) + threadIdx.x / L;
   const bool live = t < T;
   float x[V];
 #pragma unroll
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   griddep_wait();
   griddep_launch();
   const int l = threadIdx.x % L;
-  const int t = (blockIdx.x * (kRouteWarps * 32) + threadIdx.x) / L;
+  const int t = blockIdx.x * (kRouteWarps * 32 / L) + threadIdx.x / L;
   const bool live = t < T;
   int id = -1;
   float w = 0.f, dw = 0.f;

@@ -426,9 +426,10 @@ cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cu
   return by_dtype(dtype, [&](auto t) {
     using T = decltype(t);
     const int chunks = p.C / 8;
-    if (p.rows <= kNormDirectRows) {
-      int wpr = 1;
-      while (wpr * 32 < chunks) wpr *= 2;
+    int wide = 1;   // warps of a row at one chunk a lane
+    while (wide * 32 < chunks) wide *= 2;
+    if (p.rows * wide <= kNormDirectWarps) {
+      const int wpr = wide;
       const int rpb = wpr < 4 ? 4 / wpr : 1;
       return launch_pdl(k_norm_residual_direct<T>, dim3((unsigned)((p.rows + rpb - 1) / rpb)),
                         dim3(wpr * rpb * 32), 0, st, p, wpr);

@@ -267,7 +267,9 @@ MLPS = [
     (3, 64, 4, 128, 136, True, 0.0), (40, 8, 2, 128, 256, True, 1.0), (100, 4, 3, 64, 520, True, 1.0),
     (150, 3, 2, 192, 128, False, 1.0), (300, 2, 1, 64, 320, True, 0.0), (513, 2, 2, 64, 64, True, 0.5),
     (700, 1, 1, 136, 72, True, 0.0), (260, 512, 1, 64, 64, True, 1.0), (30, 4, 2, 16, 24, True, 1.0),
-    (1500, 4, 2, 64, 128, True, 2.0),
+    (1500, 4, 2, 64, 128, True, 2.0), (50, 3, 3, 96, 264, True, 0.5), (2, 6, 3, 1288, 2056, True, 0.0),
+    (8, 2, 1, 64, 72, False, 0.0), (1, 2, 2, 64, 10240, True, 0.0), (1, 3, 1, 10248, 64, True, 0.0),
+    (130, 1, 1, 72, 136, True, 0.0), (257, 1, 1, 64, 264, True, 0.0),
 ]
 
 
@@ -300,19 +302,21 @@ def test_expert_mlp_strided_rows_and_no_weights():
     assert torch.equal(wide[2, :, :C], want) and (wide[:, :, C:] == 5.0).all()
 
 
-def test_expert_mlp_nothing_routed():
-    T, E, k, C, H = 70, 4, 2, 64, 128
+@pytest.mark.parametrize("T", [3, 30, 70, 700])
+def test_expert_mlp_nothing_routed(T):
+    E, k, C, H = 4, 2, 64, 128
     v = _mlp_inputs(T, E, k, C, H, 2)
     ids = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
     v["weight"][:] = float("nan")
     assert torch.equal(_mlp(L.make_expert_cfg(T, E, k, C=C, hidden=H), v, ids), v["residual"])
 
 
-def test_expert_mlp_bad_ids_count_as_none():
-    T, E, k, C, H = 50, 4, 2, 64, 128
+@pytest.mark.parametrize("T", [4, 50])
+def test_expert_mlp_bad_ids_count_as_none(T):
+    E, k, C, H = 4, 2, 64, 128
     v = _mlp_inputs(T, E, k, C, H, 3)
     ids = _ids(T, E, k, 4)
-    ids[7, 0] = 99
+    ids[T - 2, 0], ids[1, 1] = 99, -5
     out = _mlp(L.make_expert_cfg(T, E, k, C=C, hidden=H), v, ids)
     assert L.sparsesam_device_status() == L.SS_EINDEX
     _check_mlp(v, ids, out)
@@ -320,20 +324,31 @@ def test_expert_mlp_bad_ids_count_as_none():
 
 def test_expert_mlp_a_poisoned_token_stays_alone():
     """A token of infinities and NaN reaches no other token, not even in its own tile."""
-    T, E, k, C, H = 64, 2, 1, 64, 128
-    v = _mlp_inputs(T, E, k, C, H, 5)
-    ids = _ids(T, E, k, 6, gone=0.0)
-    cfg = L.make_expert_cfg(T, E, k, C=C, hidden=H)
-    want = _mlp(cfg, v, ids)
-    v["x"][9, 3], v["x"][9, 4] = float("inf"), float("nan")
-    out = _mlp(cfg, v, ids)
-    keep = [t for t in range(T) if t != 9]
-    assert torch.equal(out[keep], want[keep]) and torch.isnan(out[9]).all()
+    E, k, C, H = 2, 1, 64, 128
+    for T in (8, 64, 100, 300):
+        v = _mlp_inputs(T, E, k, C, H, 5)
+        ids = _ids(T, E, k, 6, gone=0.0)
+        cfg = L.make_expert_cfg(T, E, k, C=C, hidden=H)
+        want = _mlp(cfg, v, ids)
+        v["x"][5, 3], v["x"][5, 4] = float("inf"), float("nan")
+        out = _mlp(cfg, v, ids)
+        keep = [t for t in range(T) if t != 5]
+        assert torch.equal(out[keep], want[keep]) and torch.isnan(out[5]).all()
 
 
-def test_two_streams_and_a_captured_graph():
+def test_expert_mlp_the_same_expert_twice():
+    """A token that names one expert twice gets it twice; more assignments than an expert has rows."""
+    for T in (2, 90):
+        E, k, C, H = 3, 3, 64, 128
+        v = _mlp_inputs(T, E, k, C, H, 15)
+        ids = torch.tensor([[1, 1, 1], [2, 0, 2]] * (T // 2), dtype=torch.int32, device="cuda")
+        _check_mlp(v, ids, _mlp(L.make_expert_cfg(T, E, k, C=C, hidden=H), v, ids))
+
+
+@pytest.mark.parametrize("T", [3, 200, 900])
+def test_two_streams_and_a_captured_graph(T):
     """Two calls at once with a workspace each, and a captured one replayed with new inputs."""
-    T, E, k, C, H = 200, 8, 2, 128, 256
+    E, k, C, H = 8, 2, 128, 256
     cfg = L.make_expert_cfg(T, E, k, C=C, hidden=H)
     a, b = _mlp_inputs(T, E, k, C, H, 7), _mlp_inputs(T, E, k, C, H, 8)
     ia, ib = _ids(T, E, k, 9), _ids(T, E, k, 10)

@@ -269,6 +269,28 @@ def test_constant_rows_and_infinities():
     assert abs(stats[1, 1].item() - 1e3) <= 1e3 * 2 * S
 
 
+def test_a_spoiled_call_leaves_nothing_behind():
+    """A call on NaN rows, then one whose workers have an odd row left over: shared memory still holds
+    the NaN where that row's partner would be."""
+    C = 1024
+    for rows in (1777, 3):
+        v = _inputs(rows, C, "bf16", "layer", rows, True, True, True, True, seed=4)
+        cfg = _cfg(rows, C, "bf16", "layer", rows, True)
+        x_out, n, stats = _forward(cfg, v, True)
+        dx_out, dn = torch.randn_like(x_out), torch.randn_like(x_out)
+        want = _backward(cfg, v, x_out, stats, dx_out, dn)
+        big = _inputs(4000, C, "bf16", "layer", 4000, True, True, True, True)
+        nan = torch.full_like(big["x"], float("nan"))
+        bcfg = _cfg(4000, C, "bf16", "layer", 4000, True)
+        _backward(bcfg, {**big, "y": nan}, nan, torch.full((4000, 4), float("nan"), device="cuda"), nan, nan)
+        got = _backward(cfg, v, x_out, stats, dx_out, dn)
+        torch.cuda.synchronize()
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+        for k in want[2]:
+            assert torch.equal(want[2][k], got[2][k]), k
+        _check_backward(v, rows, "layer", "bf16", x_out, dx_out, dn, *got)
+
+
 def test_no_rows():
     v = _inputs(0, 64, "bf16", "layer", 4, True, True, True, True)
     cfg = _cfg(0, 64, "bf16", "layer", 4, True)
