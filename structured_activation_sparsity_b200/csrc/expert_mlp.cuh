@@ -360,6 +360,11 @@ constexpr int kVecRows = 4;                    // weight rows of a warp
 constexpr int kVecSpan = 5;                    // chunks a lane of each, at most
 constexpr int kVecMostK = 8 * 32 * kVecSpan * 8;
 
+// Warps an SM. At five chunks a lane one warp more a scheduler is worth what it spills (C 1280, hidden 5120, one
+// token of two experts: 16.6 us, 19.8 with 16 warps: then not all blocks are resident at once); at four it is
+// not (9.5 us for four experts of C 768, hidden 2048, 11.3 with 20).
+__host__ __device__ constexpr int vec_warps(int V) { return V == kVecSpan ? 20 : 16; }
+
 struct ExpertVec {
   const uint16_t* x;        // fc1: [tokens, ld]; fc2: hidden rows [n, K]
   const int32_t* ids;       // [n]
@@ -461,7 +466,7 @@ __device__ __forceinline__ float vec_bias(const ExpertVec& g, int e, int row) {
 
 // hidden[a] = GELU(W1_e x[a / topk] + b1_e), rounded to bf16. WARPS of a block: kw a group of four features.
 template <int V, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, vec_warps(V) / WARPS)
     k_expert_vec_fc1(const ExpertVec g, int* status) {
   __shared__ float part[WARPS * kVecRows][WARPS];   // [row][piece]
   griddep_wait();
@@ -494,7 +499,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 
 // out[t] = residual[t] + sum_j weight[t, j] (W2_e hidden[t, j] + b2_e), the sum in the order of j.
 template <int V, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, vec_warps(V) / WARPS)
     k_expert_vec_fc2(const ExpertVec g, int* status) {
   constexpr int kRows = kVecRows / 2;                      // channels of a warp
   __shared__ float part[kMaxTopk][WARPS * kRows][WARPS];   // [expert][row][piece]
