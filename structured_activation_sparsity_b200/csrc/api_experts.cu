@@ -123,7 +123,7 @@ int sparsesam_norm_residual(const ss_norm_cfg* cfg, const void* y, const void* x
   p.n = n;
   p.stats = stats;
   p.rows = cfg->rows;
-  p.rows_per_gate = gate ? cfg->rows_per_gate : cfg->rows;
+  p.rows_per_gate = gate && cfg->rows_per_gate < cfg->rows ? cfg->rows_per_gate : cfg->rows;
   p.ld_y = or_C(cfg->ld_y, cfg->C);
   p.ld_x = or_C(cfg->ld_x, cfg->C);
   p.ld_n = or_C(cfg->ld_n, cfg->C);
@@ -204,7 +204,7 @@ int sparsesam_norm_residual_backward(const ss_norm_cfg* cfg, const void* y, cons
   p.gate_partial =
       gate ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + gate_off) : nullptr;
   p.rows = cfg->rows;
-  p.rows_per_gate = gate ? cfg->rows_per_gate : (cfg->rows > 0 ? cfg->rows : 1);
+  p.rows_per_gate = gate && cfg->rows_per_gate < cfg->rows ? cfg->rows_per_gate : cfg->rows;
   p.ld_y = or_C(cfg->ld_y, cfg->C);
   p.ld_x = or_C(cfg->ld_x, cfg->C);
   p.ld_n = or_C(cfg->ld_n, cfg->C);

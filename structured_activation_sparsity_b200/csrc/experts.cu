@@ -465,25 +465,31 @@ __global__ void __launch_bounds__(256, kCombineCtas)
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
-  const long long items = (long long)tokens * parts, step = (long long)gridDim.x * 8;
+  // Item (token t, part): the warps take every (8 grid)-th, stepped without a division.
+  const int warps = gridDim.x * 8, step_t = warps / parts, step_part = warps % parts;
   const int chunks = C / 8;
   if (K > 0) topk = K;
-  auto lookup = [&](long long item, int& p, float& w) {
+  auto lookup = [&](int t, int& p, float& w) {
     p = -1;
     w = 0.f;
-    if (item < items && lane < topk) {
-      const long long a = item / parts * topk + lane;
+    if (t < tokens && lane < topk) {
+      const long long a = (long long)t * topk + lane;
       p = row_slot(slot, a, tokens * topk, status);
       w = weight ? __ldg(weight + a) : 1.f;
     }
   };
-  long long item = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int item = blockIdx.x * 8 + (threadIdx.x >> 5);
+  int t = item / parts, part = item % parts;
   int my;
   float my_w;
-  lookup(item, my, my_w);
-  for (; item < items; item += step) {
-    const long long t = item / parts;
-    const int c0 = (int)(item - t * parts) * 32 * U + lane;
+  lookup(t, my, my_w);
+  while (t < tokens) {
+    const int c0 = part * 32 * U + lane;
+    int next_t = t + step_t, next_part = part + step_part;
+    if (next_part >= parts) {
+      next_part -= parts;
+      ++next_t;
+    }
     int next;
     float next_w;
     Chunk<T> res[U];
@@ -491,7 +497,7 @@ __global__ void __launch_bounds__(256, kCombineCtas)
     for (int i = 0; i < U; ++i) {
       chunk_zero(res[i]);
       if (residual && c0 + 32 * i < chunks)
-        chunk_load(res[i], residual + t * ld + (c0 + 32 * i) * 8);
+        chunk_load(res[i], residual + (size_t)t * ld + (c0 + 32 * i) * 8);
     }
     constexpr int kJ = K > 0 ? K : 4;   // experts whose rows are in flight together
     Chunk<T> y[kJ][U];
@@ -526,11 +532,11 @@ __global__ void __launch_bounds__(256, kCombineCtas)
       for (int q = 0; q < 8; ++q) acc[q] += r[q];
       Chunk<T> o;
       chunk_round(o, acc);
-      chunk_store(out + t * ld + (c0 + 32 * i) * 8, o);
+      chunk_store(out + (size_t)t * ld + (c0 + 32 * i) * 8, o);
     };
     if constexpr (K > 0) {
       load(0);
-      lookup(item + step, next, next_w);
+      lookup(next_t, next, next_w);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         float acc[8] = {};
@@ -541,13 +547,15 @@ __global__ void __launch_bounds__(256, kCombineCtas)
       float acc[U][8] = {};
       for (int j0 = 0; j0 < topk; j0 += kJ) {
         load(j0);
-        if (j0 == 0) lookup(item + step, next, next_w);
+        if (j0 == 0) lookup(next_t, next, next_w);
 #pragma unroll
         for (int i = 0; i < U; ++i) add(j0, i, acc[i]);
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) finish(i, acc[i]);
     }
+    t = next_t;
+    part = next_part;
     my = next;
     my_w = next_w;
   }

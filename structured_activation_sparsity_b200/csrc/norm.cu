@@ -77,22 +77,21 @@ __device__ __forceinline__ float f8_sum(const F8& f) {
 
 // ---- forward --------------------------------------------------------------------------------
 // A norm's mean and 1/sqrt over a row that `wpr` warps hold, V chunks a lane, n_w channels in warp w.
-// Each warp takes its sum and its sum of squared deviations from its own mean; those are joined by
+// (inv_w = 1 / n_w of this warp, 0 for none). Each warp takes its sum and its sum of squared deviations
+// from its own mean; those are joined by
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2
 // (Chan, Golub and LeVeque's update), so no large mean cancels and one meeting of the warps is enough.
 // LPR lanes share a row (fewer than 32: several rows a warp). chunk(e): whether chunk e is in the row (the
 // others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another.
+__device__ __forceinline__ float row_held(int C, int w, int V) {   // n_w: a span of V * 256 channels
+  const int left = C - w * V * 256;
+  return (float)(left > V * 256 ? V * 256 : left > 0 ? left : 0);
+}
 template <int V, int LPR, class Live, class Meet>
 __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int C, int wpr, int wr,
-                                            bool center, float eps, float2* red, Meet&& meet,
-                                            float& mean, float& rstd) {
+                                            float inv_w, bool center, float eps, float2* red,
+                                            Meet&& meet, float& mean, float& rstd) {
   const float inv_c = 1.0f / (float)C;
-  // Channels of warp w of the row: its span of V * 256.
-  auto held = [&](int w) {
-    const int left = C - w * V * 256;
-    return (float)(left > V * 256 ? V * 256 : left > 0 ? left : 0);
-  };
-  const float n_w = wpr == 1 ? (float)C : held(wr);
   float s = 0.f, m2 = 0.f;
   if (center) {
 #pragma unroll
@@ -100,7 +99,7 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
-  const uint64_t off = f2_same(n_w > 0.f ? -s / n_w : 0.f);
+  const uint64_t off = f2_same(-s * inv_w);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     F8 d;
@@ -119,7 +118,7 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
     s = m2 = 0.f;
     for (int w = 0; w < wpr; ++w) s += red[w].x;
     for (int w = 0; w < wpr; ++w) {
-      const float n = held(w);
+      const float n = row_held(C, w, V);
       const float2 r = red[w];
       const float d = center && n > 0.f ? r.x / n - s * inv_c : 0.f;
       m2 += r.y + n * d * d;
@@ -149,10 +148,14 @@ __device__ __forceinline__ void load_f8(F8& f, const void* ptr, long long at, fl
   chunk_ldg(c, static_cast<const typename T::Store*>(ptr) + at);
   f8_unpack(c, f);
 }
+// The gate row of a row (both fit 32 bits: a 64-bit division would be a tenth of the row's instructions).
+__device__ __forceinline__ long long gate_row(const NormParams& p, long long row) {
+  return (uint32_t)row / (uint32_t)p.rows_per_gate;
+}
 template <class T>
 __device__ __forceinline__ void load_gs(F8& f, const NormParams& p, long long row, int c) {
   F8 g;
-  load_f8<T>(g, p.gate, p.gate ? row / p.rows_per_gate * p.C + c : 0, 1.f);
+  load_f8<T>(g, p.gate, p.gate ? gate_row(p, row) * p.C + c : 0, 1.f);
   load_f8<T>(f, p.scale, c, 1.f);
 #pragma unroll
   for (int q = 0; q < 4; ++q) f.p[q] = f2_mul(f.p[q], g.p[q]);
@@ -189,10 +192,11 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
     load_f8<T>(w.pre_b, p.pre_b, c, 0.f);
   }
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float held = row_held(p.C, wr, 1), inv_w = held > 0.f ? 1.0f / held : 0.f;
   auto in_row = [&](int) { return col; };
   auto meet = [&] { __syncthreads(); };   // the block's rows share its barriers
   if (p.post_w) {
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, inv_w, p.center, p.eps, red[0] + warp - wr, meet, st.x,
                        st.y);
     if (live) apply_norm(v[0], st.x, st.y, w.post_w, w.post_b);
   }
@@ -203,7 +207,7 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   }
   if (p.pre_w) {
     if (!live) f8_fill(v[0], 0.f);
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, inv_w, p.center, p.eps, red[1] + warp - wr, meet, st.z,
                        st.w);
     if (live) {
       apply_norm(v[0], st.z, st.w, w.pre_w, w.pre_b);
@@ -286,6 +290,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   const int l = lane % LPR, sub = lane / LPR;
   const int mine = sub * (kSlot / kRows) + l * 8;    // in a slot; chunk e is LPR * 8 further on
   const int cl = c0 + l * 8;                        // the lane's first channel
+  const float inv_w = span > 0 ? 1.0f / (float)span : 0.f;
   auto in_row = [&](int e) { return FULL || l * 8 + e * LPR * 8 < span; };
   auto meet = [&] { named_barrier(1 + warp / wpr, wpr * 32); };
   int phase = 0;
@@ -310,11 +315,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       fetch(slot_y, p.y, p.ld_y, at + stride, &full[0][warp]);
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.post_w)
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, inv_w, p.center, p.eps, red[0] + warp - wr, meet, st.x,
                           st.y);
     const uint64_t rs = f2_same(p.post_w ? st.y : 1.f), ms = f2_same(-st.x * st.y);
     const S* gate = static_cast<const S*>(p.gate);
-    if (gate && live) gate += row / p.rows_per_gate * C;
+    if (gate && live) gate += gate_row(p, row) * C;
     S* out = static_cast<S*>(p.x_out) + row * p.ld_x;
     mbar_wait(&full[1][warp], phase, &abort_flag, status);
 #pragma unroll
@@ -349,7 +354,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     if (lane == 0 && at + stride < p.rows)
       fetch(slot_x, p.x, p.ld_x, at + stride, &full[1][warp]);
     if (p.pre_w) {
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, inv_w, p.center, p.eps, red[1] + warp - wr, meet, st.z,
                           st.w);
       const uint64_t r2 = f2_same(st.w), m2 = f2_same(-st.z * st.w);
       S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
