@@ -28,6 +28,7 @@
  * Conventions shared by every call
  *   - Pointers marked (device) are device memory owned by the caller; nothing is allocated or
  *     freed by these calls. Pointers marked (host) are host memory.
+ *   - Calls work on the current device, to which the pointers and the stream belong.
  *   - `stream` is a cudaStream_t (NULL = the legacy default stream). Every GPU call is
  *     asynchronous on it and never synchronises; results are ready when the stream is.
  *   - Arguments are validated on the host before any launch. On a validation error nothing is
@@ -491,7 +492,7 @@ size_t sparsesam_expert_mlp_workspace(const ss_expert_cfg* cfg);
  * routes nowhere (one outside [-1, experts) too, and records SS_EINDEX): a token without any gets
  * its residual. Any number of tokens, one included, spread over the experts in any way. bf16 operands, fp32
  * accumulation; the hidden rows are rounded to bf16 between the products, and so is each expert's
- * output row before it is weighted unless the second product was split along its K (a few rows). out
+ * output row before it is weighted (with few rows it stays in fp32). out
  * may be x or residual. ws (device, 256-byte aligned) >= sparsesam_expert_mlp_workspace(cfg) bytes, its
  * contents on entry do not matter; calls that may run at once need one each. */
 int sparsesam_expert_mlp(const ss_expert_cfg* cfg, const uint16_t* x, const int32_t* ids,

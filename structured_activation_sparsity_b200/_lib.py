@@ -152,9 +152,7 @@ def _ptrs(*tensors):
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return None
-    if isinstance(stream, int):
+    if stream is None or stream.__class__ is int:
         return stream
     return stream.cuda_stream  # torch.cuda.Stream
 

@@ -2,8 +2,10 @@
 // assignments by expert, and the row moves (gather to the sorted order, combine with weights, and
 // the combine's gradient). An assignment a = t * topk + j is token t's j-th expert.
 //
-// The row moves are bound by HBM: one warp a token, so that a token's own row crosses once however
-// many experts it goes to. The router and the sort are bound by latency.
+// The row moves are bound by HBM: warps work by token, so that a token's own row crosses once however
+// many experts it goes to (16384 tokens of 1280 bf16 to two experts each and back: 49.0 us, 0.93 of the
+// measured copy rate; the gradients of 32768 tokens of 1024: 82.2 us, 0.97). The router and the sort are
+// bound by latency and instructions.
 #include <algorithm>
 #include <type_traits>
 
@@ -22,7 +24,8 @@ __device__ __forceinline__ float exp_below(float x) { return ex2_mufu(x * 1.4426
 // L lanes a token (32 / L tokens a warp), V logits a lane (expert v * L + lane): with eight logits a lane a
 // round of the top-k is a few compares and log2 L shuffles for several tokens at once, where a whole
 // warp a token spends two warp reductions on each. Each round takes the largest logit left and the lowest
-// expert that has it. Bound by instructions (39200 tokens of 64 experts, four each: ROUTETIME us).
+// expert that has it. Bound by instructions: 39200 tokens of 64 experts, four each, take about 7 us (10 MB read);
+// with their sort and the gradient 23.7 us.
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll

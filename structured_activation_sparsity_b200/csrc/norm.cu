@@ -5,7 +5,10 @@
 //   x_out = x + gate[group] * scale * p         (rounded once to the rows' type)
 //   n     = pre norm of x_out as stored         (what the next block reads)
 //
-// Both directions are bound by HBM: every row is read and written once, all sums stay in fp32.
+// Every row is read and written once, all sums stay in fp32. Measured on B200 (HBM floor at the measured
+// copy rate in brackets): forward, 16384 rows of 1280 bf16 with everything on, 38.1 us (26.0); gradients,
+// 32768 rows of 1024 bf16, 80 us (62.4), 4039 rows of 1160 fp32, 34.7 us (17.4). What keeps them from the floor is
+// the latency of the rows' sums and shared memory's bandwidth, not HBM.
 #include <type_traits>
 
 #include "kernels.h"
@@ -52,7 +55,7 @@ __device__ __forceinline__ void f8_round(F8& f, typename T::Store* ptr) {
 }
 // To and from a vector of C fp32 in shared memory, channels c .. c + 7: the chunks' first halves lie side
 // by side, then their second halves, so that the lanes of a warp read 16 bytes next to each other
-// (eight consecutive floats a lane would meet in the banks: 46 instead of 35 us for the ViT-H batch).
+// (eight consecutive floats a lane would meet in the banks: 45.8 instead of 39.5 us for the ViT-H batch).
 __device__ __forceinline__ void f8_put(float* to, int C, int c, const F8& f) {
   *reinterpret_cast<ulonglong2*>(to + c / 2) = make_ulonglong2(f.p[0], f.p[1]);
   *reinterpret_cast<ulonglong2*>(to + C / 2 + c / 2) = make_ulonglong2(f.p[2], f.p[3]);
