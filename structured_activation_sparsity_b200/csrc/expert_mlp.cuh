@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     int base = 0;
     for (int e0 = 0; e0 < g.E; e0 += 32) {
       const int e = e0 + lane;
-      const int lo = e < g.E ? __ldg(g.offsets + e) : 0, hi = e < g.E ? __ldg(g.offsets + e + 1) : 0;
+      const int lo = e < g.E ? g.offsets[e] : 0, hi = e < g.E ? g.offsets[e + 1] : 0;
       int x = (hi - lo + TN - 1) / TN;
       const int own = x;
 #pragma unroll
@@ -461,7 +461,7 @@ struct VecTile {
 
 // The expert of assignment a, or -1 (one out of range is recorded).
 __device__ __forceinline__ int vec_expert(const ExpertVec& g, long long a, int* status) {
-  const int e = __ldg(g.ids + a);
+  const int e = g.ids[a];
   if (e < -1 || e >= g.E) {
     record_bad_index(status);
     return -1;
@@ -548,11 +548,11 @@ __global__ void __launch_bounds__(WARPS * 32, vec_warps(V) / WARPS)
   float acc = 0.f;
   for (int j = 0; j < g.topk; ++j) {
     const long long a = t * g.topk + j;
-    const int e = __ldg(g.ids + a);
+    const int e = g.ids[a];
     if (e < 0 || e >= g.E) continue;
     float y = 0.f;
     for (int q = 0; q < kw; ++q) y += part[j][r][q];
-    acc += (g.weight ? __ldg(g.weight + a) : 1.f) * (y + vec_bias(g, e, c));
+    acc += (g.weight ? g.weight[a] : 1.f) * (y + vec_bias(g, e, c));
   }
   const __nv_bfloat16 o = __float2bfloat16_rn(acc + res);
   g.out[t * g.ld + c] = *reinterpret_cast<const uint16_t*>(&o);

@@ -56,8 +56,8 @@ constexpr int kRouteWarps = 4;
 
 template <int V, int L>
 __global__ void __launch_bounds__(kRouteWarps * 32)
-    k_expert_route(const float* __restrict__ logits, int32_t* __restrict__ ids,
-                   float* __restrict__ weight, int T, int E, int topk, int renorm) {
+    k_expert_route(const float* logits, int32_t* ids, float* weight, int T, int E, int topk,
+                   int renorm) {
   griddep_wait();
   griddep_launch();
   const int l = threadIdx.x % L;
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int e = v * L + l;
-    x[v] = live && e < E ? open_logit(__ldg(logits + (size_t)t * E + e)) : -INFINITY;
+    x[v] = live && e < E ? open_logit(logits[(size_t)t * E + e]) : -INFINITY;
   }
   float best = group_max<L>(largest(x));
   const float top = best > -INFINITY ? best : 0.f;
@@ -107,10 +107,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 // softmax p over all open experts: dlogit_e = p_e (dw_e - sum_i dw_i w_i), dw_e = 0 if not chosen.
 template <int V, int L>
 __global__ void __launch_bounds__(kRouteWarps * 32)
-    k_expert_route_backward(const float* __restrict__ logits, const int32_t* __restrict__ ids,
-                            const float* __restrict__ weight, const float* __restrict__ dweight,
-                            float* __restrict__ dlogits, int T, int E, int topk, int renorm,
-                            int* status) {
+    k_expert_route_backward(const float* logits, const int32_t* ids, const float* weight,
+                            const float* dweight, float* dlogits, int T, int E, int topk,
+                            int renorm, int* status) {
   griddep_wait();
   griddep_launch();
   const int l = threadIdx.x % L;
@@ -119,14 +118,14 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
   int id = -1;
   float w = 0.f, dw = 0.f;
   if (live && l < topk) {
-    id = __ldg(ids + (size_t)t * topk + l);
+    id = ids[(size_t)t * topk + l];
     if (id < -1 || id >= E) {
       record_bad_index(status);
       id = -1;
     }
     if (id >= 0) {
-      w = __ldg(weight + (size_t)t * topk + l);
-      dw = __ldg(dweight + (size_t)t * topk + l);
+      w = weight[(size_t)t * topk + l];
+      dw = dweight[(size_t)t * topk + l];
     }
   }
   float d[V];
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = v * L + l;
-      d[v] = live && e < E ? open_logit(__ldg(logits + (size_t)t * E + e)) : -INFINITY;
+      d[v] = live && e < E ? open_logit(logits[(size_t)t * E + e]) : -INFINITY;
     }
     const float best = group_max<L>(largest(d)), top = best > -INFINITY ? best : 0.f;
     float total = 0.f;
@@ -226,7 +225,7 @@ __device__ __forceinline__ void sort_walk(const int32_t* ids, int a0, int a1, in
   for (int a = a0 + lane; a - lane < a1; a += 128) {
     int e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = a + 32 * i < a1 ? __ldg(ids + a + 32 * i) : -1;
+    for (int i = 0; i < 4; ++i) e[i] = a + 32 * i < a1 ? ids[a + 32 * i] : -1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (a - lane + 32 * i >= a1) break;
@@ -250,9 +249,9 @@ __device__ __forceinline__ void sort_count(const int32_t* ids, int a0, int a1, i
   });
 }
 
-__global__ void __launch_bounds__(kSortThreads) k_expert_count(const int32_t* __restrict__ ids,
-                                                               int32_t* __restrict__ hist, int n,
-                                                               int chunk, int E, int* status) {
+__global__ void __launch_bounds__(kSortThreads) k_expert_count(const int32_t* ids, int32_t* hist,
+                                                               int n, int chunk, int E,
+                                                               int* status) {
   extern __shared__ int counts[];   // [warps][E]
   griddep_wait();
   griddep_launch();
@@ -272,9 +271,8 @@ __global__ void __launch_bounds__(kSortThreads) k_expert_count(const int32_t* __
 }
 
 __global__ void __launch_bounds__(kSortThreads)
-    k_expert_place(const int32_t* __restrict__ ids, const int32_t* __restrict__ hist,
-                   int32_t* __restrict__ order, int32_t* __restrict__ slot,
-                   int32_t* __restrict__ offsets, int n, int chunk, int E, int* status) {
+    k_expert_place(const int32_t* ids, const int32_t* hist, int32_t* order, int32_t* slot,
+                   int32_t* offsets, int n, int chunk, int E, int* status) {
   extern __shared__ int counts[];   // [warps][E]: counts, then the next place of each expert
   __shared__ int2 s_part[kSortThreads];
   __shared__ int s_sum[kSortWarps];
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(kSortThreads)
     if (part_of < parts) {
 #pragma unroll 16
       for (int b = part_of; b < gridDim.x; b += parts) {
-        const int h = __ldg(hist + (size_t)b * E + ex);
+        const int h = hist[(size_t)b * E + ex];
         sum += h;
         sum_before += b < blockIdx.x ? h : 0;
       }
@@ -397,7 +395,7 @@ cudaError_t launch_expert_place(const int32_t* ids, const int32_t* hist, int32_t
 // ---- row moves ------------------------------------------------------------------------------
 // The sorted place of assignment a, or -1 (none; one outside [-1, n) is recorded and skipped).
 __device__ __forceinline__ int row_slot(const int32_t* slot, long long a, int n, int* status) {
-  const int p = __ldg(slot + a);
+  const int p = slot[a];
   if (p < -1 || p >= n) {
     record_bad_index(status);
     return -1;
@@ -408,9 +406,8 @@ __device__ __forceinline__ int row_slot(const int32_t* slot, long long a, int n,
 // xs[slot[t, j]] = x[t]: the token's row is loaded once, up to eight chunks a lane in flight.
 template <class T>
 __global__ void __launch_bounds__(256)
-    k_expert_gather(const typename T::Store* __restrict__ x, const int32_t* __restrict__ slot,
-                    typename T::Store* __restrict__ xs, int tokens, int topk, int C, long long ld,
-                    int* status) {
+    k_expert_gather(const typename T::Store* x, const int32_t* slot, typename T::Store* xs,
+                    int tokens, int topk, int C, long long ld, int* status) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -461,10 +458,9 @@ constexpr int kCombineCtas = 3;   // CTAs an SM
 
 template <class T, int U, int K>
 __global__ void __launch_bounds__(256, kCombineCtas)
-    k_expert_combine(const typename T::Store* __restrict__ ys, const int32_t* __restrict__ slot,
-                     const float* __restrict__ weight, const typename T::Store* residual,
-                     typename T::Store* out, int tokens, int topk, int C, long long ld, int parts,
-                     int* status) {
+    k_expert_combine(const typename T::Store* ys, const int32_t* slot, const float* weight,
+                     const typename T::Store* residual, typename T::Store* out, int tokens,
+                     int topk, int C, long long ld, int parts, int* status) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -478,7 +474,7 @@ __global__ void __launch_bounds__(256, kCombineCtas)
     if (t < tokens && lane < topk) {
       const long long a = (long long)t * topk + lane;
       p = row_slot(slot, a, tokens * topk, status);
-      w = weight ? __ldg(weight + a) : 1.f;
+      w = weight ? weight[a] : 1.f;
     }
   };
   const int item = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -566,10 +562,9 @@ __global__ void __launch_bounds__(256, kCombineCtas)
 
 // The same over fp32 partials [splits][tokens * topk][C] of fc2's k-splits, added in split order; one chunk a lane.
 __global__ void __launch_bounds__(256)
-    k_expert_combine_splits(const float* __restrict__ ys, const int32_t* __restrict__ slot,
-                            const float* __restrict__ weight, const uint16_t* residual,
-                            uint16_t* out, int tokens, int topk, int C, long long ld, int parts,
-                            int splits, int* status) {
+    k_expert_combine_splits(const float* ys, const int32_t* slot, const float* weight,
+                            const uint16_t* residual, uint16_t* out, int tokens, int topk, int C,
+                            long long ld, int parts, int splits, int* status) {
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31;
@@ -580,7 +575,7 @@ __global__ void __launch_bounds__(256)
   float my_w = 0.f;
   if (lane < topk) {
     my = row_slot(slot, (long long)t * topk + lane, tokens * topk, status);
-    my_w = weight ? __ldg(weight + (size_t)t * topk + lane) : 1.f;
+    my_w = weight ? weight[(size_t)t * topk + lane] : 1.f;
   }
   float acc[8];
 #pragma unroll
@@ -675,11 +670,10 @@ cudaError_t launch_expert_combine(const void* ys, const int32_t* slot, const flo
 // U chunks a lane at a time, all their loads in flight together.
 template <class T, int U>
 __global__ void __launch_bounds__(256)
-    k_expert_combine_backward(const typename T::Store* __restrict__ dout,
-                              const typename T::Store* ys, const int32_t* __restrict__ slot,
-                              const float* __restrict__ weight, typename T::Store* dys,
-                              float* __restrict__ dweight, int tokens, int topk, int C,
-                              long long ld, int* status) {
+    k_expert_combine_backward(const typename T::Store* dout, const typename T::Store* ys,
+                              const int32_t* slot, const float* weight, typename T::Store* dys,
+                              float* dweight, int tokens, int topk, int C, long long ld,
+                              int* status) {
   constexpr int K = 2;
   griddep_wait();
   griddep_launch();
@@ -690,7 +684,7 @@ __global__ void __launch_bounds__(256)
   float my_w = 0.f;
   if (lane < topk) {
     my = row_slot(slot, (long long)t * topk + lane, tokens * topk, status);
-    my_w = __ldg(weight + (size_t)t * topk + lane);
+    my_w = weight[(size_t)t * topk + lane];
   }
   const int chunks = C / 8;
   float my_dw = 0.f;

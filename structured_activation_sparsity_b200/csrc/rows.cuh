@@ -56,7 +56,9 @@ __device__ __forceinline__ void chunk_load(Chunk<T>& c, const typename T::Store*
     c.w[4 * i + 3] = v.w;
   }
 }
-// The same from global memory that nothing writes while the kernel runs (parameters).
+// The same from global memory that no kernel here writes (parameters): the read-only path may run ahead of
+// griddep_wait(). What a kernel before it may have written (rows, routes, orders) is loaded plainly, through
+// pointers without __restrict__, and so stays behind the wait.
 template <class T>
 __device__ __forceinline__ void chunk_ldg(Chunk<T>& c, const typename T::Store* p) {
 #pragma unroll
