@@ -269,6 +269,7 @@ MLPS = [
     (700, 1, 1, 136, 72, True, 0.0), (260, 512, 1, 64, 64, True, 1.0), (30, 4, 2, 16, 24, True, 1.0),
     (1500, 4, 2, 64, 128, True, 2.0), (50, 3, 3, 96, 264, True, 0.5), (2, 6, 3, 1288, 2056, True, 0.0),
     (8, 2, 1, 64, 72, False, 0.0), (1, 2, 2, 64, 10240, True, 0.0), (1, 3, 1, 10248, 64, True, 0.0),
+    (30, 4, 2, 8, 8, True, 1.0), (12, 4, 2, 64, 1024, True, 0.0), (3, 5, 2, 8, 16, False, 0.0),
     (130, 1, 1, 72, 136, True, 0.0), (257, 1, 1, 64, 264, True, 0.0),
 ]
 
@@ -452,3 +453,63 @@ def test_training_through_the_routed_rows():
         # fp32 throughout: a few hundred roundings of 2^-24 in sums of |terms| near 1e3; the
         # difference's own error is near 1e-7
         assert abs(mine - want) <= 1e-4 * max(1.0, np.abs(f64(got) * v).sum()), (mine, want)
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 channels of sorted rows, and of logits."""
+    T, k, C = 70000, 4, 8192
+    n = T * k
+    assert n * C > 1 << 31
+    cfg = L.make_expert_cfg(T, 8, k, C=C)
+    slot = torch.randperm(n, device="cuda", dtype=torch.int32).view(T, k)
+    x = torch.randn(T, C, device="cuda", dtype=torch.bfloat16)
+    xs = torch.full((n, C), 7.0, device="cuda", dtype=torch.bfloat16)
+    L.sparsesam_expert_gather(cfg, x, slot, xs)
+    for t0 in range(0, T, 10000):
+        want = x[t0:t0 + 10000]
+        for j in range(k):
+            assert torch.equal(xs[slot[t0:t0 + 10000, j].long()], want)
+    # k equal rows weighted 2^-2, 2^-1, 2^-3, 2^-3: their sum is the row, exactly
+    w = torch.tensor([0.25, 0.5, 0.125, 0.125], device="cuda").expand(T, k).contiguous()
+    out = torch.full_like(x, 7.0)
+    L.sparsesam_expert_combine(cfg, xs, slot, w, None, out)
+    assert torch.equal(out, x)
+    dw = torch.full((T, k), 7.0, device="cuda")
+    L.sparsesam_expert_combine_backward(cfg, x, xs, slot, w, xs, dw)
+    for t0 in range(0, T, 10000):
+        want = x[t0:t0 + 10000]
+        for j in range(k):
+            assert torch.equal(xs[slot[t0:t0 + 10000, j].long()], want * w[0, j].item())
+        sq = (want.double() ** 2).sum(1, keepdim=True)      # all terms of the dot product are positive
+        assert ((dw[t0:t0 + 10000] - sq).abs() <= (C / 32 + 8) * F * sq).all()
+    del xs, x, out
+    T, E = (1 << 22) + 300, 512
+    assert T * E > 1 << 31
+    lg = torch.zeros(T, E, device="cuda")
+    hot = torch.randint(0, E, (T, 1), device="cuda")
+    lg.scatter_(1, hot, 1.0)
+    ids, weight = _route(lg, 1, 1)
+    assert torch.equal(ids, hot.int()) and (weight == 1.0).all()
+    dl = torch.full_like(lg, 7.0)
+    L.sparsesam_expert_route_backward(L.make_expert_cfg(T, E, 1), lg, 1, ids, weight, weight, dl)
+    assert not dl.any()
+    assert L.sparsesam_device_status() == L.SS_OK
+
+
+@pytest.mark.parametrize("T", [2, 30])
+def test_expert_mlp_weights_past_32_bits(T):
+    """Each weight tensor holds more than 2^31 values; the last experts work as in a call with them alone."""
+    E, C, H = 512, 2048, 2056
+    assert E * C * H > 1 << 31
+    v = _mlp_inputs(T, 2, 1, C, H, 5)
+    ids = torch.arange(T, device="cuda", dtype=torch.int32)[:, None] % 2
+    big = dict(v)
+    for name in ("w1", "w2"):
+        big[name] = torch.zeros(E, *v[name].shape[1:], device="cuda", dtype=torch.bfloat16)
+    for name in ("b1", "b2"):
+        big[name] = torch.zeros(E, v[name].shape[1], device="cuda", dtype=torch.bfloat16)
+    for name in ("w1", "w2", "b1", "b2"):
+        big[name][-2:] = v[name]
+    out = _mlp(L.make_expert_cfg(T, E, 1, C=C, hidden=H), big, ids + E - 2)
+    assert L.sparsesam_device_status() == L.SS_OK
+    _check_mlp(v, ids, out)

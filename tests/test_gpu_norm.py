@@ -327,3 +327,33 @@ def test_captured_and_on_another_stream():
             assert torch.equal(a, b)
         for k in grads:
             assert grads[k] is None or torch.equal(grads[k], want[2][k])
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 channels: the last rows, and the sums over all of them where the rows repeat."""
+    C, part = 2048, 512
+    rows = (1 << 20) + 3 * part
+    assert rows * C > 1 << 31
+    small = _inputs(part, C, "bf16", "layer", part, True, True, True, True)
+    many = rows // part
+    tile = lambda t: t.repeat(many, 1)  # noqa: E731
+    v = {**small, "x": tile(small["x"]), "y": tile(small["y"])}
+    cfg = _cfg(rows, C, "bf16", "layer", rows, True)
+    x_out, n, stats = _forward(cfg, v, True, x_out=v["x"], n=torch.full_like(v["x"], 7.0))
+    torch.cuda.synchronize()
+    for at in (0, (1 << 20) - part, rows - part):
+        s = slice(at, at + part)
+        _check_forward(small, part, "layer", "bf16", x_out[s], n[s], stats[s])
+    for s in range(part, rows, part):
+        assert torch.equal(x_out[s:s + part], x_out[:part]) and torch.equal(n[s:s + part], n[:part])
+    del n
+    dx_out, dn = torch.randn_like(small["x"]), torch.randn_like(small["x"])
+    big = tile(dx_out)
+    dx, dy, g = _backward(cfg, v, x_out, stats, big, tile(dn), dx=big, dy=v["y"])
+    torch.cuda.synchronize()
+    one = _backward(_cfg(part, C, "bf16", "layer", part, True), small, x_out[:part].clone(),
+                    stats[:part].clone(), dx_out, dn)
+    _check_backward(small, part, "layer", "bf16", x_out[:part], dx_out, dn, *one)
+    for s in range(0, rows, part):
+        assert torch.equal(dx[s:s + part], dx[:part]) and torch.equal(dy[s:s + part], dy[:part])
+    assert torch.equal(dx[-part:], one[0]) and torch.equal(dy[-part:], one[1])
