@@ -6,7 +6,7 @@
 //   n     = pre norm of x_out as stored         (what the next block reads)
 //
 // Every row is read and written once, all sums stay in fp32. Measured on B200 (HBM floor at the measured
-// copy rate in brackets): forward, 16384 rows of 1280 bf16 with everything on, 38.1 us (26.0); gradients,
+// copy rate in brackets): forward, 16384 rows of 1280 bf16 with everything on, 30.5 us (26.0); gradients,
 // 32768 rows of 1024 bf16, 80 us (62.4), 4039 rows of 1160 fp32, 34.7 us (17.4). What keeps them from the floor is
 // the latency of the rows' sums and shared memory's bandwidth, not HBM.
 #include <type_traits>
@@ -220,20 +220,28 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   if (p.stats && live && c == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
 }
 
-// Many rows: a persistent CTA of 24 warps an SM; `wpr` warps hold a row, each a span of it with V chunks
+// Many rows: a persistent CTA of 16 warps an SM; `wpr` warps hold a row, each a span of it with V chunks
 // of eight channels a lane, so that a row's sums cost a few shuffles per V chunks and nothing waits for
 // another warp at wpr == 1. Every warp has a slot of shared memory for its y and one for its x, which
 // bulk copies fill with the next row's as soon as this one's values are read: the memory stays busy
-// without registers for it, and 80 registers a thread leave room for the 24 warps that hide the sums'
-// latency. The parameters sit in shared memory in fp32 (scale folded into the post norm's); the gate,
-// which changes with the row, is read from L1. LPR < 32: narrow rows, 32 / LPR of them a warp. FULL: every
-// lane's V chunks are in the row.
-constexpr int kFwdWarps = 24, kFwdThreads = 32 * kFwdWarps;
+// without registers for it. The parameters sit in shared memory in fp32 (scale folded into the post
+// norm's); the gate, which changes with the row, is read from L1. LPR < 32: narrow rows, 32 / LPR of them
+// a warp. kFull: every lane's V chunks are in the row; kFullOne: and the row is one warp's, so that its
+// width is known.
+// 16384 rows of 1280 bf16: 38.2 us with 24 warps of 80 registers, 36.1 with the width known (which spills
+// less), 32.8 with 20 warps, 30.5 with 16 (128 registers), 31.8 with 12; two rows ahead a warp 33.1 (their shared
+// memory comes out of the L1 that holds the gate).
+constexpr int kFwdWarps = 16, kFwdThreads = 32 * kFwdWarps;
+static_assert(kFwdWarps % 4 == 0, "rows of up to four warps");
 
-template <class T, int V, int LPR, bool FULL>
-__global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormParams p, int wpr,
+enum NormSpan { kRagged, kFull, kFullOne };
+
+template <class T, int V, int LPR, NormSpan SPAN>
+__global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormParams p, int warps,
                                                                   int* status) {
   using S = typename T::Store;
+  constexpr bool FULL = SPAN != kRagged;
+  const int wpr = SPAN == kFullOne ? 1 : warps, C = SPAN == kFullOne ? V * LPR * 8 : p.C;
   constexpr int kRows = 32 / LPR;                   // rows a warp holds
   constexpr int kSlot = kRows * V * LPR * 8;        // elements of a warp's y or x
   extern __shared__ __align__(128) uint8_t smem[];
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   float* prm = reinterpret_cast<float*>(smem + 2 * kFwdWarps * kSlot * sizeof(S));
   // prm [4][C]: scale * post_w, scale * post_b, pre_w, pre_b
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int wr = warp % wpr, C = p.C;
+  const int wr = warp % wpr;
   if (threadIdx.x < 2 * kFwdWarps) mbar_init(&full[0][0] + threadIdx.x, 1);
   if (threadIdx.x == 0) abort_flag = 0;
   fence_barrier_init();
@@ -417,8 +425,10 @@ static NormShape norm_shape(long long rows, int C, int es, int tensors, int R) {
 
 template <class T, int V, int LPR>
 static cudaError_t launch_fwd(const NormParams& p, int wpr, int* status, cudaStream_t st) {
-  const auto kernel = p.C == V * LPR * wpr * 8 ? k_norm_residual<T, V, LPR, true>
-                                               : k_norm_residual<T, V, LPR, false>;
+  // (A row of fewer than 32 lanes has one warp.)
+  const auto kernel = p.C != V * LPR * wpr * 8 ? k_norm_residual<T, V, LPR, kRagged>
+                      : wpr == 1               ? k_norm_residual<T, V, LPR, kFullOne>
+                                 : k_norm_residual<T, V, LPR, LPR == 32 ? kFull : kFullOne>;
   const size_t smem = (size_t)2 * kFwdWarps * V * 32 * 8 * sizeof(typename T::Store) +
                       (size_t)4 * p.C * sizeof(float);
   const cudaError_t e =
@@ -444,16 +454,20 @@ cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cu
     }
     if (chunks <= 8) return launch_fwd<T, 1, 8>(p, 1, status, st);
     if (chunks <= 16) return launch_fwd<T, 1, 16>(p, 1, status, st);
-    // The fewest warps a row with at most 40 values a lane (fp32: 24, for the slots' size).
-    constexpr int kMost = T::kWords == 8 ? 3 : 5;
+    // The fewest warps a row with at most 64 values a lane (fp32: 40, for the slots' size): 16384 rows of
+    // 2048 bf16 take 46.3 us with one warp a row, 59.0 with two; of 4096 fp32 229 with four, 284 with eight.
+    constexpr int kMost = T::kWords == 8 ? 5 : 8;
     int wpr = 1;
     while (chunks > 32 * kMost * wpr) wpr *= 2;
     switch ((chunks + 32 * wpr - 1) / (32 * wpr)) {
       case 1: return launch_fwd<T, 1, 32>(p, wpr, status, st);
       case 2: return launch_fwd<T, 2, 32>(p, wpr, status, st);
       case 3: return launch_fwd<T, 3, 32>(p, wpr, status, st);
-      case 4: return launch_fwd<T, kMost < 4 ? 3 : 4, 32>(p, wpr, status, st);
-      default: return launch_fwd<T, kMost < 5 ? 3 : 5, 32>(p, wpr, status, st);
+      case 4: return launch_fwd<T, 4, 32>(p, wpr, status, st);
+      case 5: return launch_fwd<T, 5, 32>(p, wpr, status, st);
+      case 6: return launch_fwd<T, kMost < 6 ? 5 : 6, 32>(p, wpr, status, st);
+      case 7: return launch_fwd<T, kMost < 7 ? 5 : 7, 32>(p, wpr, status, st);
+      default: return launch_fwd<T, kMost < 8 ? 5 : 8, 32>(p, wpr, status, st);
     }
   });
 }

@@ -107,6 +107,16 @@ CASES = [
     (19, 1288, "bf16", "layer", 4, False, False, False, False),
     (4000, 64, "bf16", "layer", 3, True, True, False, True),
     (9001, 40, "f16", "rms", 9001, True, True, True, True),
+    # one warp a row, more, ragged: the spans of the many-row kernel
+    (3500, 1280, "bf16", "layer", 100, True, True, True, True),
+    (1300, 2048, "bf16", "rms", 650, True, True, False, True),
+    (1100, 1800, "f16", "layer", 100, True, False, True, True),
+    (700, 4096, "bf16", "layer", 350, True, True, True, True),
+    (900, 1160, "f32", "layer", 300, True, True, True, True),
+    (400, 3880, "f32", "rms", 400, True, True, True, True),
+    (300, 4096, "f32", "layer", 7, True, True, True, True),
+    (1400, 1536, "f16", "layer", 200, False, True, True, True),
+    (2500, 512, "f32", "layer", 500, True, True, False, False),
 ]
 IDS = ["-".join(map(str, c[:5])) for c in CASES]
 
