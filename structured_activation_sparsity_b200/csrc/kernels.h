@@ -215,9 +215,10 @@ struct NormParams {
   float eps;
 };
 // Up to this many warps of rows (one per 256 channels, rounded up to a power of two), the forward takes the
-// direct kernel. Measured on B200, direct / persistent: C 1280, 148 rows 4.4 / 9.0 us, 512 rows 8.5 / 9.1, 1024
-// rows 15.5 / 9.2; C 64, 2048 rows 3.6 / 4.7, 4096 rows 5.5 / 4.8; C 4096, 148 rows 6.9 / 9.5, 512 rows 23.9 / 10.2.
-constexpr int kNormDirectWarps = 4096;
+// direct kernel. Measured on B200, direct / persistent: bf16 C 1280, 256 rows 4.5 / 5.7 us, 512 rows 8.0 / 5.7,
+// 1024 rows 14.6 / 5.7; C 64, 2048 rows 3.3 / 3.8, 4096 rows 5.0 / 4.0; C 4096, 148 rows 6.6 / 10.5, 256 rows
+// 12.0 / 10.6; fp32 C 1160, 256 rows 4.8 / 9.8, 512 rows 8.4 / 9.9.
+constexpr int kNormDirectWarps = 2560;
 cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cudaStream_t st);
 
 struct NormBwdParams {
