@@ -9,11 +9,11 @@
 // (tcgen05 cta_group::2), each bringing its half of both operands.
 //
 // Measured on B200: 16384 tokens x 2 of 8 experts, C 1280, hidden 5120: fc1 358 us, fc2 304 us (1.20 and 1.41
-// PFLOP/s; the measured cuBLAS burst is 1.63, sustained 1.38); the whole call 767 us in a burst, 854 back to
+// PFLOP/s; the measured cuBLAS burst is 1.63, sustained 1.38); the whole call 767 us in a burst, 833 back to
 // back under the power cap. 784 tokens x 2 of 16 experts, C 1024, hidden 4096, 98 rows an expert: 38 us a
-// product, whose weights take HBM 20.8 us. Every k-block of that is some 250 rows of 128 bytes through the
-// load unit, many from different pages; asking for the weights ahead in L2, as tiles or as whole rows, made
-// it slower (89 to 98 us instead of 82).
+// product, whose weights take HBM 20.8 us. Loading those weights alone in the same boxes takes 28.8 us shared
+// evenly and 32.9 in whole tiles (a plain read 22.6), the token rows 2 more; asking for the weights ahead in
+// L2, as tiles or as whole rows, made it slower (89 to 98 us instead of 82 for the call).
 //
 // The row counts are on the device only (the sort's offsets): every CTA turns them into the same
 // list of tiles, and takes units (tile, feature tile, k-split) c, c + grid, c + 2 grid, ...
