@@ -80,10 +80,12 @@ __device__ __forceinline__ float f8_sum(const F8& f) {
 
 // ---- forward --------------------------------------------------------------------------------
 // A norm's mean and 1/sqrt over a row that `wpr` warps hold, V chunks a lane, n_w channels in warp w.
-// (inv_w = 1 / n_w of this warp, 0 for none). Each warp takes its sum and its sum of squared deviations
+// (held = n_w of this warp). Each warp takes its sum and its sum of squared deviations
 // from its own mean; those are joined by
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2
 // (Chan, Golub and LeVeque's update), so no large mean cancels and one meeting of the warps is enough.
+// The means are divisions, not products with 1 / n: a constant row whose sum is exact has exactly its
+// value as the mean, and no deviations that 1 / sqrt(eps) would make large.
 // LPR lanes share a row (fewer than 32: several rows a warp). chunk(e): whether chunk e is in the row (the
 // others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another.
 __device__ __forceinline__ float row_held(int C, int w, int V) {   // n_w: a span of V * 256 channels
@@ -92,17 +94,19 @@ __device__ __forceinline__ float row_held(int C, int w, int V) {   // n_w: a spa
 }
 template <int V, int LPR, class Live, class Meet>
 __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int C, int wpr, int wr,
-                                            float inv_w, bool center, float eps, float2* red,
+                                            float held, bool center, float eps, float2* red,
                                             Meet&& meet, float& mean, float& rstd) {
-  const float inv_c = 1.0f / (float)C;
+  const float n_c = (float)C, inv_c = 1.0f / n_c;
   float s = 0.f, m2 = 0.f;
+  mean = 0.f;
   if (center) {
 #pragma unroll
     for (int e = 0; e < V; ++e) s += f8_sum(v[e]);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (held > 0.f) mean = s / held;
   }
-  const uint64_t off = f2_same(-s * inv_w);
+  const uint64_t off = f2_same(-mean);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     F8 d;
@@ -119,22 +123,26 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
     if ((threadIdx.x & 31) == 0) red[wr] = make_float2(s, m2);
     meet();
     s = m2 = 0.f;
-    for (int w = 0; w < wpr; ++w) s += red[w].x;
     for (int w = 0; w < wpr; ++w) {
-      const float n = row_held(C, w, V);
       const float2 r = red[w];
-      const float d = center && n > 0.f ? r.x / n - s * inv_c : 0.f;
-      m2 += r.y + n * d * d;
+      s += r.x;
+      m2 += r.y;
+    }
+    if (center) {
+      mean = s / n_c;
+      for (int w = 0; w < wpr; ++w) {
+        const float n = row_held(C, w, V);
+        const float d = n > 0.f ? red[w].x / n - mean : 0.f;
+        m2 += n * d * d;
+      }
     }
   }
-  mean = center ? s * inv_c : 0.f;
   rstd = rsqrtf(m2 * inv_c + eps);
 }
 
-// The norm and residual arithmetic of one chunk, the same in both kernels.
-struct NormWeights {   // the parameters of a thread's eight channels
-  F8 post_w, post_b, gs, pre_w, pre_b;   // gs = gate * scale
-};
+// The norm of one chunk, (v - mean) rstd w + b, the same in both kernels. (The mean goes first: v rstd - mean
+// rstd is one instruction less, but rounds at the size of mean rstd, which a constant row of 1000 and
+// an eps of 1e-6 make 1e6.)
 __device__ __forceinline__ void apply_norm(F8& v, float mean, float rstd, const F8& w, const F8& b) {
   const uint64_t m = f2_same(-mean), r = f2_same(rstd);
 #pragma unroll
@@ -155,13 +163,18 @@ __device__ __forceinline__ void load_f8(F8& f, const void* ptr, long long at, fl
 __device__ __forceinline__ long long gate_row(const NormParams& p, long long row) {
   return (uint32_t)row / (uint32_t)p.rows_per_gate;
 }
+// The post norm's parameters times the residual scale.
 template <class T>
-__device__ __forceinline__ void load_gs(F8& f, const NormParams& p, long long row, int c) {
-  F8 g;
-  load_f8<T>(g, p.gate, p.gate ? gate_row(p, row) * p.C + c : 0, 1.f);
-  load_f8<T>(f, p.scale, c, 1.f);
+__device__ __forceinline__ void load_scaled(F8& w, F8& b, const NormParams& p, int c) {
+  F8 k;
+  load_f8<T>(k, p.scale, c, 1.f);
+  load_f8<T>(w, p.post_w, c, 1.f);
+  load_f8<T>(b, p.post_b, c, 0.f);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) f.p[q] = f2_mul(f.p[q], g.p[q]);
+  for (int q = 0; q < 4; ++q) {
+    w.p[q] = f2_mul(w.p[q], k.p[q]);
+    b.p[q] = f2_mul(b.p[q], k.p[q]);
+  }
 }
 
 // Few rows: `wpr` warps a row, one chunk of eight channels a thread, everything loaded at once. What
@@ -178,8 +191,7 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   const bool live = col && row < p.rows;
   griddep_wait();
   griddep_launch();
-  NormWeights w;
-  F8 v[1], x;
+  F8 v[1], x, gate, post_w, post_b, pre_w, pre_b;
   f8_fill(v[0], 0.f);
   f8_fill(x, 0.f);
   if (live) {
@@ -188,32 +200,30 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
     chunk_load(xr, static_cast<const S*>(p.x) + row * p.ld_x + c);
     f8_unpack(yr, v[0]);
     f8_unpack(xr, x);
-    load_gs<T>(w.gs, p, row, c);
-    load_f8<T>(w.post_w, p.post_w, c, 1.f);
-    load_f8<T>(w.post_b, p.post_b, c, 0.f);
-    load_f8<T>(w.pre_w, p.pre_w, c, 1.f);
-    load_f8<T>(w.pre_b, p.pre_b, c, 0.f);
+    load_f8<T>(gate, p.gate, p.gate ? gate_row(p, row) * p.C + c : 0, 1.f);
+    load_f8<T>(pre_w, p.pre_w, c, 1.f);
+    load_f8<T>(pre_b, p.pre_b, c, 0.f);
+    load_scaled<T>(post_w, post_b, p, c);   // (last: its products wait for their loads)
   }
   float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float held = row_held(p.C, wr, 1), inv_w = held > 0.f ? 1.0f / held : 0.f;
+  const float held = row_held(p.C, wr, 1);
   auto in_row = [&](int) { return col; };
   auto meet = [&] { __syncthreads(); };   // the block's rows share its barriers
-  if (p.post_w) {
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, inv_w, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+  if (p.post_w)
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
                        st.y);
-    if (live) apply_norm(v[0], st.x, st.y, w.post_w, w.post_b);
-  }
   if (live) {
+    apply_norm(v[0], st.x, p.post_w ? st.y : 1.f, post_w, post_b);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) v[0].p[q] = f2_fma(v[0].p[q], w.gs.p[q], x.p[q]);
+    for (int q = 0; q < 4; ++q) v[0].p[q] = f2_fma(v[0].p[q], gate.p[q], x.p[q]);
     f8_round<T>(v[0], static_cast<S*>(p.x_out) + row * p.ld_x + c);
   }
   if (p.pre_w) {
     if (!live) f8_fill(v[0], 0.f);
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, inv_w, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
                        st.w);
     if (live) {
-      apply_norm(v[0], st.z, st.w, w.pre_w, w.pre_b);
+      apply_norm(v[0], st.z, st.w, pre_w, pre_b);
       f8_store<T>(static_cast<S*>(p.n) + row * p.ld_n + c, v[0]);
     }
   }
@@ -281,15 +291,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     fetch(slot_x, p.x, p.ld_x, first, &full[1][warp]);
   }
   for (int c = threadIdx.x * 8; c < C; c += kFwdThreads * 8) {
-    F8 a, b, k;
-    load_f8<T>(k, p.scale, c, 1.f);
-    load_f8<T>(a, p.post_w, c, 1.f);
-    load_f8<T>(b, p.post_b, c, 0.f);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      a.p[q] = f2_mul(a.p[q], k.p[q]);
-      b.p[q] = f2_mul(b.p[q], k.p[q]);
-    }
+    F8 a, b;
+    load_scaled<T>(a, b, p, c);
     f8_put(prm, C, c, a);
     f8_put(prm + C, C, c, b);
     load_f8<T>(a, p.pre_w, c, 1.f);
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   const int l = lane % LPR, sub = lane / LPR;
   const int mine = sub * (kSlot / kRows) + l * 8;    // in a slot; chunk e is LPR * 8 further on
   const int cl = c0 + l * 8;                        // the lane's first channel
-  const float inv_w = span > 0 ? 1.0f / (float)span : 0.f;
+  const float held = (float)span;
   auto in_row = [&](int e) { return FULL || l * 8 + e * LPR * 8 < span; };
   auto meet = [&] { named_barrier(1 + warp / wpr, wpr * 32); };
   int phase = 0;
@@ -326,9 +329,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       fetch(slot_y, p.y, p.ld_y, at + stride, &full[0][warp]);
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.post_w)
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, inv_w, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
                           st.y);
-    const uint64_t rs = f2_same(p.post_w ? st.y : 1.f), ms = f2_same(-st.x * st.y);
+    const float rstd = p.post_w ? st.y : 1.f;
     const S* gate = static_cast<const S*>(p.gate);
     if (gate && live) gate += gate_row(p, row) * C;
     S* out = static_cast<S*>(p.x_out) + row * p.ld_x;
@@ -348,9 +351,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       f8_unpack(t, x);
       f8_get(w, prm, C, c);
       f8_get(b, prm + C, C, c);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        v[e].p[q] = f2_fma(f2_fma(v[e].p[q], rs, ms), w.p[q], b.p[q]);
+      apply_norm(v[e], st.x, rstd, w, b);
       if (gate) {
         load_f8<T>(w, gate, c, 1.f);
 #pragma unroll
@@ -365,9 +366,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     if (lane == 0 && at + stride < p.rows)
       fetch(slot_x, p.x, p.ld_x, at + stride, &full[1][warp]);
     if (p.pre_w) {
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, inv_w, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
                           st.w);
-      const uint64_t r2 = f2_same(st.w), m2 = f2_same(-st.z * st.w);
       S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -377,9 +377,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
         F8 w, b;
         f8_get(w, prm + 2 * C, C, c);
         f8_get(b, prm + 3 * C, C, c);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          v[e].p[q] = f2_fma(f2_fma(v[e].p[q], r2, m2), w.p[q], b.p[q]);
+        apply_norm(v[e], st.z, st.w, w, b);
         f8_store<T>(nrow + c, v[e]);
       }
     }
@@ -717,11 +715,11 @@ __global__ void __launch_bounds__(kNormThreads, 1)
         read(h[i], 2, i);
         read(dn[i], 3, i);
         const float2 t = reinterpret_cast<const float2*>(stat + i)[1];
-        const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
+        const uint64_t rs = f2_same(t.y), m = f2_same(-t.x);   // (the mean first: see apply_norm)
         uint64_t s1 = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
+          h[i].p[q] = f2_mul(f2_add(h[i].p[q], m), rs);
           acc_pw.p[q] = f2_fma(dn[i].p[q], h[i].p[q], acc_pw.p[q]);
           acc_pb.p[q] = f2_add(acc_pb.p[q], dn[i].p[q]);
           dn[i].p[q] = f2_mul(dn[i].p[q], w_pre.p[q]);
@@ -755,9 +753,9 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       if (FULL || col) f8_store<T>(dx + i * p.ld_x, D[i]);
       if constexpr (POST) {
         const float2 t = *reinterpret_cast<const float2*>(stat + i);
-        const uint64_t rs = f2_same(t.y), ms = f2_same(-t.x * t.y);
+        const uint64_t rs = f2_same(t.y), m = f2_same(-t.x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[i].p[q] = f2_fma(h[i].p[q], rs, ms);
+        for (int q = 0; q < 4; ++q) h[i].p[q] = f2_mul(f2_add(h[i].p[q], m), rs);
       }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
