@@ -46,6 +46,24 @@ def test_route_far_logits(E, k, renorm):
     assert (np.abs(G.f64(dlg) - want) <= size * (2 * (64 + 32 + 64) * G.F * prob + 16 * 2.0 ** -149)).all()
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_huge_logits(renorm):
+    """Logits whose steps are larger than any distance that counts, with closed ones among them. (The last
+    row's third weight is e^-128 = 2.6e-56, less than half of fp32's least step: 0, off by itself.)"""
+    inf, big = float("inf"), 3.4028234663852886e38
+    lg = torch.tensor([[-big, -inf, -big, -inf], [1e30, 1e30, -1e30, 0.0], [big, -big, 0.0, -inf],
+                       [-1e30, -inf, -1.0000001e30, -big], [1e9, 1e9 - 64, 1e9 - 128, 0.0]], device="cuda")
+    ids, w = G._route(lg, 3, renorm)
+    want_ids, want = X.route(G.f64(lg), 3, renorm)
+    assert np.array_equal(ids.cpu().numpy(), want_ids)
+    assert (np.abs(G.f64(w) - want) <= 64 * G.F * want + 2.0 ** -150).all()
+    dw = torch.tensor([[1.0, -2.0, 0.5]] * 5, device="cuda")
+    dlg = torch.full_like(lg, 7.0)
+    L.sparsesam_expert_route_backward(L.make_expert_cfg(5, 4, 3), lg, renorm, ids, w, dw, dlg)
+    want = X.route_backward(G.f64(lg), 3, renorm, G.f64(dw))
+    assert (np.abs(G.f64(dlg) - want) <= 4 * 160 * G.F * (np.abs(want) + (want != 0))).all()
+
+
 def test_route_backward_of_an_infinite_logit():
     """A logit of +inf makes the softmax NaN, and so the gradient of every open expert, while closed
     experts (-inf, NaN) have 0 and other tokens their own."""
