@@ -440,7 +440,8 @@ int sparsesam_expert_route(const ss_expert_cfg* cfg, const float* logits, int32_
 /* Gradient of weight for the logits: dweight (device) fp32 [tokens, topk] -> dlogits (device) fp32
  * [tokens, experts], every entry written. logits, ids, weight as the forward had and wrote them (logits
  * may be NULL with renorm). dweight at an id of -1 is not read; an id outside [-1, experts) records
- * SS_EINDEX and counts as -1. */
+ * SS_EINDEX and counts as -1. Without renorm, a row with a logit of +inf has NaN at every open expert;
+ * closed ones have 0. */
 int sparsesam_expert_route_backward(const ss_expert_cfg* cfg, const float* logits, int32_t renorm,
                                     const int32_t* ids, const float* weight, const float* dweight,
                                     float* dlogits, void* stream);

@@ -180,9 +180,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     }
     const float best = group_max<L>(largest(d)), top = best > -INFINITY ? best : 0.f;
     const float total = group_sum<L>(exps_below(d, top, d));
-    const float k = total > 0.f ? -mean / total : 0.f;
+    const float k = total == 0.f ? 0.f : -mean / total;   // (0: every expert is closed)
 #pragma unroll
     for (int v = 0; v < V; ++v) d[v] *= k;
+    if (total != total) {
+      // A logit of +inf: the softmax is NaN, and so is every open expert's gradient, a closed one's 0.
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int e = v * L + l;
+        d[v] = live && e < E && open_logit(logits[(size_t)t * E + e]) > -INFINITY ? total : 0.f;
+      }
+    }
   }
   const float add = renorm ? w * (dw - mean) : w * dw;
   for (int j = 0; j < topk; ++j) {
