@@ -324,13 +324,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
         f8_unpack(t, v[e]);
       }
     }
-    __syncwarp();
-    if (lane == 0 && at + stride < p.rows)
-      fetch(slot_y, p.y, p.ld_y, at + stride, &full[0][warp]);
+    // The next row may come into a slot only when every lane has its values in registers, not merely asked
+    // for them: after work that used them (the row's sums, or x_out's stores), and with the reads
+    // ordered before the copies by the proxy fence. (Right after the loads, a queue of the other
+    // warps' reads let the copies win: rows with channels of the row 592 further on.)
+    auto fetch_next = [&](S* to, const void* src, long long ld, uint64_t* bar) {
+      if (lane == 0 && at + stride < p.rows) fetch(to, src, ld, at + stride, bar);
+    };
+    auto slots_read = [&] {
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.post_w)
+    if (p.post_w) {
       row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
                           st.y);
+      slots_read();
+      fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
+    }
     const float rstd = p.post_w ? st.y : 1.f;
     const S* gate = static_cast<const S*>(p.gate);
     if (gate && live) gate += gate_row(p, row) * C;
@@ -362,9 +373,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       }
       f8_round<T>(v[e], out + c);
     }
-    __syncwarp();
-    if (lane == 0 && at + stride < p.rows)
-      fetch(slot_x, p.x, p.ld_x, at + stride, &full[1][warp]);
+    slots_read();
+    if (!p.post_w) fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
+    fetch_next(slot_x, p.x, p.ld_x, &full[1][warp]);
     if (p.pre_w) {
       row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
                           st.w);
@@ -696,8 +707,10 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       else chunk_zero(t);
       f8_unpack(t, f);
     };
-    // The last meeting of the worker's warps also frees the stage: every thread has its chunks.
+    // The last meeting of the worker's warps also frees the stage: every thread has its chunks, its reads
+    // ordered before the copies that come in their place.
     auto release = [&] {
+      fence_proxy_async_smem();
       meet();
       if (last && tw == 0 && ahead < r1) {
         fetch(ahead, st);
@@ -705,7 +718,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       }
     };
     F8 D[N], h[N];
-    float a[N], b[N];
+    float a[N], b[N], rstd[N];
     if constexpr (PRE) {
       F8 dn[N], w_pre;
       if (FULL || col) f8_get(w_pre, kept, p.C, c);
@@ -753,6 +766,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       if (FULL || col) f8_store<T>(dx + i * p.ld_x, D[i]);
       if constexpr (POST) {
         const float2 t = *reinterpret_cast<const float2*>(stat + i);
+        rstd[i] = t.y;
         const uint64_t rs = f2_same(t.y), m = f2_same(-t.x);
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[i].p[q] = f2_mul(f2_add(h[i].p[q], m), rs);
@@ -772,9 +786,6 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       }
     }
     if constexpr (POST) {
-      float rstd[N];
-#pragma unroll
-      for (int i = 0; i < N; ++i) rstd[i] = stat[i].y;
       worker_sums(a, b, release);
 #pragma unroll
       for (int i = 0; i < N; ++i) {

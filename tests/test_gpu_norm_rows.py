@@ -48,3 +48,56 @@ def test_constant_rows_cancel(rows, C, dtype):
     _, _, g = N._backward(cfg, both, v["y"], stats, d[0], d[1])
     assert (g["dpost_w"] == 0).all() and (g["dpre_w"] == 0).all()
     assert L.sparsesam_device_status() == L.SS_OK
+
+
+# rows of several rounds of the many-row kernels (16, 8 or 4 rows a CTA at a time), with each norm alone and both
+ROUNDS = [(800, 4096, "f32"), (1500, 2560, "f32"), (3000, 4096, "bf16"), (3000, 2056, "f16"),
+          (5000, 1280, "bf16"), (9000, 256, "f32"), (30000, 64, "bf16")]
+
+
+@pytest.mark.parametrize("norms", ["post", "pre", "both", "none"])
+@pytest.mark.parametrize("rows,C,dtype", ROUNDS, ids=lambda v: str(v))
+def test_no_row_meets_the_next_one(rows, C, dtype, norms):
+    """Copies of later rows go into the shared memory that a row is read from. With constant rows of very
+    different values, exact sums and exact outputs, a single channel of another row shows. (fp32 gradients'
+    column sums of constant rows and of gradients that are small whole numbers are exact as well.)"""
+    dt = N.TORCH[dtype]
+    col = torch.tensor([0.0, 1.0, -3.0, 1000.0, 30720.0, 0.109375, -251.0])[torch.arange(rows) % 7]
+    col = col.to(dt).cuda()[:, None]
+    flat, zero = col.expand(rows, C).contiguous(), torch.zeros(rows, C, dtype=dt, device="cuda")
+    post, pre = norms in ("post", "both"), norms in ("pre", "both")
+    v = N._inputs(rows, C, dtype, "layer", rows, post, False, False, pre, seed=3)
+    v["y"], v["x"] = flat, zero
+    cfg = N._cfg(rows, C, dtype, "layer", rows, False)
+    want = v["post_b"].expand(rows, C) if post else flat
+    for _ in range(20):
+        x_out, n, stats = N._forward(cfg, v, pre)
+        assert torch.equal(x_out, want)
+        if post:
+            assert torch.equal(stats[:, 0], col[:, 0].float())
+        elif pre:
+            assert torch.equal(stats[:, 2], col[:, 0].float()) and torch.equal(n, v["pre_b"].expand(rows, C))
+    # gradients: dx_out and dn whole numbers -1, 0, 1 along the rows
+    d = ((torch.arange(rows) % 3) - 1).to(dt).cuda()[:, None].expand(rows, C).contiguous()
+    scaled = {**v, "scale": torch.ones(C, dtype=dt, device="cuda")}
+    for key in ("post_w", "pre_w"):
+        if v[key] is not None:
+            scaled[key] = torch.ones(C, dtype=dt, device="cuda")
+    for key in ("post_b", "pre_b"):
+        scaled[key] = None
+    st = torch.zeros(rows, 4, device="cuda")
+    st[:, 0], st[:, 2], st[:, 1], st[:, 3] = col[:, 0].float(), col[:, 0].float(), 1.0, 1.0
+    total = d.double().sum(0).float()
+    for _ in range(20):
+        dx, dy, g = N._backward(cfg, scaled, flat, st, d, d if pre else None)
+        # a constant gradient of a norm: g - mean(g) = 0 (LayerNorm), so D = d with or without the pre norm
+        assert torch.equal(dx, d)
+        if post:
+            assert (dy == 0).all() and (g["dpost_w"] == 0).all() and (g["dscale"] == 0).all()
+        else:
+            assert torch.equal(dy, d)
+            big = (d.double() * flat.double()).sum(0)
+            assert ((g["dscale"].double() - big).abs() <= rows * 2.0 ** -24 * (d * flat).double().abs().sum(0)).all()
+        if pre:
+            assert (g["dpre_w"] == 0).all()
+    assert L.sparsesam_device_status() == L.SS_OK
