@@ -87,15 +87,16 @@ __device__ __forceinline__ float f8_sum(const F8& f) {
 // The means are divisions, not products with 1 / n: a constant row whose sum is exact has exactly its
 // value as the mean, and no deviations that 1 / sqrt(eps) would make large.
 // LPR lanes share a row (fewer than 32: several rows a warp). chunk(e): whether chunk e is in the row (the
-// others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another.
+// others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another;
+// used(): called when a sum over the warp has used every lane's values.
 __device__ __forceinline__ float row_held(int C, int w, int V) {   // n_w: a span of V * 256 channels
   const int left = C - w * V * 256;
   return (float)(left > V * 256 ? V * 256 : left > 0 ? left : 0);
 }
-template <int V, int LPR, class Live, class Meet>
+template <int V, int LPR, class Live, class Meet, class Used>
 __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int C, int wpr, int wr,
                                             float held, bool center, float eps, float2* red,
-                                            Meet&& meet, float& mean, float& rstd) {
+                                            Meet&& meet, Used&& used, float& mean, float& rstd) {
   const float n_c = (float)C, inv_c = 1.0f / n_c;
   float s = 0.f, m2 = 0.f;
   mean = 0.f;
@@ -104,6 +105,7 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
     for (int e = 0; e < V; ++e) s += f8_sum(v[e]);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    used();
     if (held > 0.f) mean = s / held;
   }
   const uint64_t off = f2_same(-mean);
@@ -119,6 +121,7 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
+  if (!center) used();
   if (wpr > 1) {
     if ((threadIdx.x & 31) == 0) red[wr] = make_float2(s, m2);
     meet();
@@ -156,7 +159,7 @@ __device__ __forceinline__ void load_f8(F8& f, const void* ptr, long long at, fl
     return;
   }
   Chunk<T> c;
-  chunk_ldg(c, static_cast<const typename T::Store*>(ptr) + at);
+  chunk_load(c, static_cast<const typename T::Store*>(ptr) + at);
   f8_unpack(c, f);
 }
 // The gate row of a row (both fit 32 bits: a 64-bit division would be a tenth of the row's instructions).
@@ -210,8 +213,8 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   auto in_row = [&](int) { return col; };
   auto meet = [&] { __syncthreads(); };   // the block's rows share its barriers
   if (p.post_w)
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
-                       st.y);
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, [] {},
+                       st.x, st.y);
   if (live) {
     apply_norm(v[0], st.x, p.post_w ? st.y : 1.f, post_w, post_b);
 #pragma unroll
@@ -220,8 +223,8 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   }
   if (p.pre_w) {
     if (!live) f8_fill(v[0], 0.f);
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
-                       st.w);
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, [] {},
+                       st.z, st.w);
     if (live) {
       apply_norm(v[0], st.z, st.w, pre_w, pre_b);
       f8_store<T>(static_cast<S*>(p.n) + row * p.ld_n + c, v[0]);
@@ -336,21 +339,34 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       __syncwarp();
     };
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.post_w) {
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
-                          st.y);
-      slots_read();
-      fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
-    }
+    if (p.post_w)
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, [&] {
+        slots_read();
+        fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
+      }, st.x, st.y);
     const float rstd = p.post_w ? st.y : 1.f;
     const S* gate = static_cast<const S*>(p.gate);
     if (gate && live) gate += gate_row(p, row) * C;
     S* out = static_cast<S*>(p.x_out) + row * p.ld_x;
+    // The gate's chunks come together ahead of the loop's stores, as far as the registers hold them. (One by
+    // one between the stores, as plain loads must stay, the ViT-H batch took 37.4 us instead of 31.8, and
+    // 2048 channels 54.6 instead of 47.8 in halves; with several warps a row and seven or eight chunks a
+    // lane, what spills costs more: 16384 x 4096 bf16 129 us in halves, 116 one by one.)
+    constexpr int kAhead = SPAN == kFullOne ? (V > 7 ? V / 2 : V) : (V > 6 ? 1 : V);
+    Chunk<T> gates[kAhead];
+    auto load_gates = [&](int e0) {
+      if (!gate) return;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (e0 + i < V && live && in_row(e0 + i)) chunk_load(gates[i], gate + cl + (e0 + i) * LPR * 8);
+    };
+    load_gates(0);
     mbar_wait(&full[1][warp], phase, &abort_flag, status);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       // (one chunk's operands at a time: gathering them ahead would cost the registers)
       asm volatile("" ::: "memory");
+      if (e > 0 && e % kAhead == 0) load_gates(e);
       if (!live || !in_row(e)) {
         f8_fill(v[e], 0.f);
         continue;
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       f8_get(b, prm + C, C, c);
       apply_norm(v[e], st.x, rstd, w, b);
       if (gate) {
-        load_f8<T>(w, gate, c, 1.f);
+        f8_unpack(gates[e % kAhead], w);
 #pragma unroll
         for (int q = 0; q < 4; ++q) v[e].p[q] = f2_fma(v[e].p[q], w.p[q], x.p[q]);
       } else {
@@ -377,8 +393,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     if (!p.post_w) fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
     fetch_next(slot_x, p.x, p.ld_x, &full[1][warp]);
     if (p.pre_w) {
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
-                          st.w);
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, [] {},
+                          st.z, st.w);
       S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
 #pragma unroll
       for (int e = 0; e < V; ++e) {

@@ -56,9 +56,11 @@ __device__ __forceinline__ void chunk_load(Chunk<T>& c, const typename T::Store*
     c.w[4 * i + 3] = v.w;
   }
 }
-// The same from global memory that no kernel here writes (parameters): the read-only path may run ahead of
-// griddep_wait(). What a kernel before it may have written (rows, routes, orders) is loaded plainly, through
-// pointers without __restrict__, and so stays behind the wait.
+// The same over the read-only path, whose loads the compiler may move ahead of griddep_wait(): only for
+// addresses that depend on something loaded plainly behind the wait (an expert's weights), or where the
+// work before the wait is known to be done. All else (rows, routes, orders, and the norms' parameters and
+// gates, which the launch before may just have written) is loaded plainly, through pointers without
+// __restrict__, and so stays behind the wait.
 template <class T>
 __device__ __forceinline__ void chunk_ldg(Chunk<T>& c, const typename T::Store* p) {
 #pragma unroll

@@ -101,3 +101,43 @@ def test_no_row_meets_the_next_one(rows, C, dtype, norms):
         if pre:
             assert (g["dpre_w"] == 0).all()
     assert L.sparsesam_device_status() == L.SS_OK
+
+@pytest.mark.parametrize("rows,C", [(20, 1280), (3000, 1280), (5200, 128), (900, 4096)])
+def test_parameters_written_by_the_call_before(rows, C):
+    """Gates are activations: gate, scale and weights that the library call just before writes, with no
+    wait in between, count as written, in the forward and in the gradient."""
+    groups, eps = 4, 1e-6
+    v = N._inputs(rows, C, "bf16", "layer", -(-rows // groups), True, True, True, True, seed=6)
+    cfg = N._cfg(rows, C, "bf16", "layer", -(-rows // groups), True)
+    big = 40000
+    src = torch.randn(big, C, device="cuda").bfloat16()
+    made = torch.empty_like(src)
+    bcfg = L.make_norm_cfg(big, C, eps=eps)
+    d = torch.randn(2, rows, C, device="cuda").bfloat16()
+    # rows of `made`: the gate rows, then scale and the norms' parameters, first and last of them
+    at = dict(scale=groups, post_w=groups + 1, post_b=big - 1, pre_w=big - 2, pre_b=big - 3)
+    v.update(gate=made[:groups], **{k: made[i] for k, i in at.items()})
+
+    def make():
+        L.sparsesam_norm_residual(bcfg, src, src, None, None, None, None, None, None, made, None, None)
+    make()
+    torch.cuda.synchronize()
+    x_out, n, stats = N._forward(cfg, v, True)
+    want = N._backward(cfg, v, x_out, stats, d[0], d[1])
+    N._check_forward(v, -(-rows // groups), "layer", "bf16", x_out, n, stats)
+    torch.cuda.synchronize()
+    for _ in range(20):
+        made.fill_(float("nan"))
+        out, n2 = torch.empty_like(x_out), torch.empty_like(n)
+        make()
+        N._forward(cfg, v, True, x_out=out, n=n2)
+        assert torch.equal(out, x_out) and torch.equal(n2, n)
+        made.fill_(float("nan"))
+        ws = torch.empty(L.sparsesam_norm_residual_backward_workspace(cfg), dtype=torch.uint8, device="cuda")
+        dx, dy = torch.empty_like(x_out), torch.empty_like(x_out)
+        grads = {k: None if t is None else torch.empty_like(t) for k, t in want[2].items()}
+        make()
+        N._backward(cfg, v, x_out, stats, d[0], d[1], dx=dx, dy=dy, grads=grads, ws=ws)
+        assert torch.equal(dx, want[0]) and torch.equal(dy, want[1])
+        for k, t in grads.items():
+            assert torch.equal(t, want[2][k]), k
