@@ -110,6 +110,14 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// After a wait that gave up: waits for what is still in flight to this barrier's phase, kWaitLimitNs at most
+// (whatever the waits' limit is set to), before its shared memory may be given up.
+__device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 < kWaitLimitNs) {
+  }
+}
+
 // mbar_wait for a barrier that another CTA of the cluster arrives on (what it did before is visible after).
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                   int* status) {

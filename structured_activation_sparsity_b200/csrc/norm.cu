@@ -310,14 +310,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   const float held = (float)span;
   auto in_row = [&](int e) { return FULL || l * 8 + e * LPR * 8 < span; };
   auto meet = [&] { named_barrier(1 + warp / wpr, wpr * 32); };
-  int phase = 0;
-  for (long long at = first; at < p.rows; at += stride, phase ^= 1) {
+  // Once a wait gave up (recorded), the lane waits no more and lane 0 asks for no more rows; the walk goes on to
+  // its end, so that no barrier is left with missing threads (the addresses do not depend on the data),
+  // and lane 0 then waits for the copies still in flight. Bit 0 of state is the row's parity; bit 1 says that a
+  // wait gave up, bits 2 and 3 then hold the parities of the slots' last copies.
+  int state = 0;
+  for (long long at = first; at < p.rows; at += stride, state ^= 1) {
     const long long row = at + sub;
     const bool live = LPR == 32 || row < p.rows;
     F8 v[V];
-    // A wait that gives up is recorded; the walk goes on to its end, so that no barrier is left with
-    // missing threads (the addresses do not depend on the data).
-    mbar_wait(&full[0][warp], phase, &abort_flag, status);
+    if (state < 2 && !mbar_wait(&full[0][warp], state, &abort_flag, status))
+      state |= 2 | state << 2 | state << 3;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       f8_fill(v[e], 0.f);
@@ -332,7 +335,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     // ordered before the copies by the proxy fence. (Right after the loads, a queue of the other
     // warps' reads let the copies win: rows with channels of the row 592 further on.)
     auto fetch_next = [&](S* to, const void* src, long long ld, uint64_t* bar) {
-      if (lane == 0 && at + stride < p.rows) fetch(to, src, ld, at + stride, bar);
+      if (lane == 0 && state < 2 && at + stride < p.rows) fetch(to, src, ld, at + stride, bar);
     };
     auto slots_read = [&] {
       fence_proxy_async_smem();
@@ -361,7 +364,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
         if (e0 + i < V && live && in_row(e0 + i)) chunk_load(gates[i], gate + cl + (e0 + i) * LPR * 8);
     };
     load_gates(0);
-    mbar_wait(&full[1][warp], phase, &abort_flag, status);
+    if (state < 2 && !mbar_wait(&full[1][warp], state, &abort_flag, status))
+      state |= 2 | (p.post_w && at + stride < p.rows ? state ^ 1 : state) << 2 | state << 3;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       // (one chunk's operands at a time: gathering them ahead would cost the registers)
@@ -411,6 +415,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     if (p.stats && live && wr == 0 && l == 0) reinterpret_cast<float4*>(p.stats)[row] = st;
     // One norm only: its next meeting must not overtake a warp that still reads this one's sums.
     if (wpr > 1 && (p.post_w == nullptr) != (p.pre_w == nullptr)) meet();
+  }
+  if (lane == 0 && state >= 2) {
+    mbar_drain(&full[0][warp], state >> 2 & 1);
+    mbar_drain(&full[1][warp], state >> 3 & 1);
   }
 }
 
@@ -577,6 +585,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     }
   };
   long long ahead = r0;
+  bool gave_up = false;   // a wait did (recorded): no more waits, no more rows asked for
   if (rl < g.rl && tw == 0)
     for (int s = 0; s < g.stages && ahead < r1; ++s, ahead += R) fetch(ahead, s);
 
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     auto release = [&] {
       fence_proxy_async_smem();
       meet();
-      if (last && tw == 0 && ahead < r1) {
+      if (last && tw == 0 && !gave_up && ahead < r1) {
         fetch(ahead, st);
         ahead += R;
       }
@@ -824,9 +833,9 @@ __global__ void __launch_bounds__(kNormThreads, 1)
     int st = 0, phase = 0;
     for (long long r = r0; r < r1; r += R) {
       const int n = (int)(r1 - r < R ? r1 - r : R);
-      // A wait that gives up is recorded; the walk goes on to its end, so that no barrier is left
-      // with missing threads (the addresses do not depend on the data).
-      mbar_wait(bar + st, phase, &abort_flag, status);
+      // After a wait that gives up the walk goes on to its end, so that no barrier is left with missing
+      // threads (the addresses do not depend on the data).
+      if (!gave_up) gave_up = !mbar_wait(bar + st, phase, &abort_flag, status);
       // Rows of one step share a gate row: a stage with a border between its rows takes a step each.
       int done = 0;
       do {
@@ -851,6 +860,11 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       }
     }
     if (p.gate) close_group();
+    if (gave_up && tw == 0) {   // the copies still in flight: of the last fetch of each stage
+      const int n = (int)((ahead - r0) / R);
+      for (int k = n > g.stages ? n - g.stages : 0; k < n; ++k)
+        mbar_drain(bar + k % g.stages, k / g.stages & 1);
+    }
   }
   // The CTA's column sums, in worker order: [pre_w, pre_b, P1, P0][C], over what the workers kept (the closed
   // groups' sums are read before they are overwritten).
