@@ -87,16 +87,15 @@ __device__ __forceinline__ float f8_sum(const F8& f) {
 // The means are divisions, not products with 1 / n: a constant row whose sum is exact has exactly its
 // value as the mean, and no deviations that 1 / sqrt(eps) would make large.
 // LPR lanes share a row (fewer than 32: several rows a warp). chunk(e): whether chunk e is in the row (the
-// others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another;
-// used(): called when a sum over the warp has used every lane's values.
+// others hold zeros); red: one float2 a warp of the row; meet(): the row's warps wait for one another.
 __device__ __forceinline__ float row_held(int C, int w, int V) {   // n_w: a span of V * 256 channels
   const int left = C - w * V * 256;
   return (float)(left > V * 256 ? V * 256 : left > 0 ? left : 0);
 }
-template <int V, int LPR, class Live, class Meet, class Used>
+template <int V, int LPR, class Live, class Meet>
 __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int C, int wpr, int wr,
                                             float held, bool center, float eps, float2* red,
-                                            Meet&& meet, Used&& used, float& mean, float& rstd) {
+                                            Meet&& meet, float& mean, float& rstd) {
   const float n_c = (float)C, inv_c = 1.0f / n_c;
   float s = 0.f, m2 = 0.f;
   mean = 0.f;
@@ -105,7 +104,6 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
     for (int e = 0; e < V; ++e) s += f8_sum(v[e]);
 #pragma unroll
     for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    used();
     if (held > 0.f) mean = s / held;
   }
   const uint64_t off = f2_same(-mean);
@@ -121,7 +119,6 @@ __device__ __forceinline__ void row_moments(const F8 (&v)[V], Live&& chunk, int 
   }
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) m2 += __shfl_xor_sync(0xffffffffu, m2, o);
-  if (!center) used();
   if (wpr > 1) {
     if ((threadIdx.x & 31) == 0) red[wr] = make_float2(s, m2);
     meet();
@@ -213,8 +210,8 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   auto in_row = [&](int) { return col; };
   auto meet = [&] { __syncthreads(); };   // the block's rows share its barriers
   if (p.post_w)
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, [] {},
-                       st.x, st.y);
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+                       st.y);
   if (live) {
     apply_norm(v[0], st.x, p.post_w ? st.y : 1.f, post_w, post_b);
 #pragma unroll
@@ -223,8 +220,8 @@ __global__ void __launch_bounds__(512) k_norm_residual_direct(const NormParams p
   }
   if (p.pre_w) {
     if (!live) f8_fill(v[0], 0.f);
-    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, [] {},
-                       st.z, st.w);
+    row_moments<1, 32>(v, in_row, p.C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+                       st.w);
     if (live) {
       apply_norm(v[0], st.z, st.w, pre_w, pre_b);
       f8_store<T>(static_cast<S*>(p.n) + row * p.ld_n + c, v[0]);
@@ -274,22 +271,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   griddep_launch();
 
   const int per_cta = kFwdWarps / wpr * kRows;
-  const long long stride = (long long)gridDim.x * per_cta;
-  const long long first = (long long)blockIdx.x * per_cta + warp / wpr * kRows;   // of the warp
+  // (rows and a step past them fit 32 bits)
+  const uint32_t rows = (uint32_t)p.rows, stride = gridDim.x * per_cta;
+  const uint32_t first = blockIdx.x * per_cta + warp / wpr * kRows;   // of the warp
   const int c0 = wr * V * LPR * 8;                  // first channel of the warp's span
   const int span = FULL || C - c0 > V * LPR * 8 ? V * LPR * 8 : C > c0 ? C - c0 : 0;
   S* slot_y = slots + (size_t)warp * 2 * kSlot;
   S* slot_x = slot_y + kSlot;
   // The warp's span of its rows from `row` on (rows kSlot / kRows apart in the slot).
-  auto fetch = [&](S* to, const void* src, long long ld, long long row, uint64_t* bar) {
-    const int n = (int)(p.rows - row < kRows ? p.rows - row : kRows);
+  auto fetch = [&](S* to, const void* src, long long ld, uint32_t row, uint64_t* bar) {
+    const int n = rows - row < kRows ? (int)(rows - row) : kRows;
     mbar_expect_tx(bar, (uint32_t)(n * span * (int)sizeof(S)));
     if (span > 0)
       for (int i = 0; i < n; ++i)
         bulk_load(to + i * (kSlot / kRows), static_cast<const S*>(src) + (row + i) * ld + c0,
                   (uint32_t)(span * (int)sizeof(S)), bar);
   };
-  if (lane == 0 && first < p.rows) {
+  if (lane == 0 && first < rows) {
     fetch(slot_y, p.y, p.ld_y, first, &full[0][warp]);
     fetch(slot_x, p.x, p.ld_x, first, &full[1][warp]);
   }
@@ -315,9 +313,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
   // and lane 0 then waits for the copies still in flight. Bit 0 of state is the row's parity; bit 1 says that a
   // wait gave up, bits 2 and 3 then hold the parities of the slots' last copies.
   int state = 0;
-  for (long long at = first; at < p.rows; at += stride, state ^= 1) {
-    const long long row = at + sub;
-    const bool live = LPR == 32 || row < p.rows;
+  for (uint32_t at = first; at < rows; at += stride, state ^= 1) {
+    const uint32_t row = at + sub;
+    const bool live = LPR == 32 || row < rows;
     F8 v[V];
     if (state < 2 && !mbar_wait(&full[0][warp], state, &abort_flag, status))
       state |= 2 | state << 2 | state << 3;
@@ -330,32 +328,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
         f8_unpack(t, v[e]);
       }
     }
-    // The next row may come into a slot only when every lane has its values in registers, not merely asked
-    // for them: after work that used them (the row's sums, or x_out's stores), and with the reads
-    // ordered before the copies by the proxy fence. (Right after the loads, a queue of the other
-    // warps' reads let the copies win: rows with channels of the row 592 further on.)
+    // The next row may come into a slot only behind the proxy fence, which orders every lane's reads before
+    // the copies. (A warp barrier alone lets the copies win against a queue of reads: rows with channels
+    // of the row 592 further on.)
     auto fetch_next = [&](S* to, const void* src, long long ld, uint64_t* bar) {
-      if (lane == 0 && state < 2 && at + stride < p.rows) fetch(to, src, ld, at + stride, bar);
+      if (lane == 0 && state < 2 && at + stride < rows) fetch(to, src, ld, at + stride, bar);
     };
     auto slots_read = [&] {
       fence_proxy_async_smem();
       __syncwarp();
     };
+    slots_read();
+    fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
     float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.post_w)
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, [&] {
-        slots_read();
-        fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
-      }, st.x, st.y);
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[0] + warp - wr, meet, st.x,
+                          st.y);
     const float rstd = p.post_w ? st.y : 1.f;
     const S* gate = static_cast<const S*>(p.gate);
     if (gate && live) gate += gate_row(p, row) * C;
     S* out = static_cast<S*>(p.x_out) + row * p.ld_x;
     // The gate's chunks come together ahead of the loop's stores, as far as the registers hold them. (One by
     // one between the stores, as plain loads must stay, the ViT-H batch took 37.4 us instead of 31.8, and
-    // 2048 channels 54.6 instead of 47.8 in halves; with several warps a row and seven or eight chunks a
-    // lane, what spills costs more: 16384 x 4096 bf16 129 us in halves, 116 one by one.)
-    constexpr int kAhead = SPAN == kFullOne ? (V > 7 ? V / 2 : V) : (V > 6 ? 1 : V);
+    // 2048 channels 54.6 instead of 47.8 in halves. With several warps a row what spills costs more:
+    // six chunks a lane 101 us, two at a time 87, 16384 x 4096 bf16 128 two at a time, 119 one by one.)
+    constexpr int kAhead = SPAN == kFullOne ? (V > 7 ? V / 2 : V) : V > 6 ? 1 : V > 4 ? 2 : V;
     Chunk<T> gates[kAhead];
     auto load_gates = [&](int e0) {
       if (!gate) return;
@@ -365,7 +362,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
     };
     load_gates(0);
     if (state < 2 && !mbar_wait(&full[1][warp], state, &abort_flag, status))
-      state |= 2 | (p.post_w && at + stride < p.rows ? state ^ 1 : state) << 2 | state << 3;
+      state |= 2 | (at + stride < rows ? state ^ 1 : state) << 2 | state << 3;
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       // (one chunk's operands at a time: gathering them ahead would cost the registers)
@@ -394,11 +391,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_norm_residual(const NormPara
       f8_round<T>(v[e], out + c);
     }
     slots_read();
-    if (!p.post_w) fetch_next(slot_y, p.y, p.ld_y, &full[0][warp]);
     fetch_next(slot_x, p.x, p.ld_x, &full[1][warp]);
     if (p.pre_w) {
-      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, [] {},
-                          st.z, st.w);
+      row_moments<V, LPR>(v, in_row, C, wpr, wr, held, p.center, p.eps, red[1] + warp - wr, meet, st.z,
+                          st.w);
       S* nrow = static_cast<S*>(p.n) + row * p.ld_n;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
