@@ -309,16 +309,6 @@ __device__ __forceinline__ bool pair_tile_full(int c0, const AttnParams& P) {
   return (P.b * kStripes) % (2 * kBM) == 0 && c0 + kBN <= P.N;
 }
 
-// If the CTA gave up a wait, a bounded pause lets its copies and MMAs still in flight land before
-// its shared memory and TMEM are released.
-__device__ __forceinline__ void abort_drain(volatile int* abort) {
-  if (*abort) {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 50000ull) {
-    }
-  }
-}
-
 // Row `row` of O (TMEM, DH fp32 columns at t_o) into registers: every 16-column load issued
 // before the one wait (a TMEM load takes a few hundred cycles; one after another they add up).
 template <int DH>

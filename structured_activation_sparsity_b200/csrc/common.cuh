@@ -118,6 +118,16 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// The same without a barrier to ask: if the CTA gave up a wait, a bounded pause lets its copies and MMAs still in flight land before
+// its shared memory and TMEM are released.
+__device__ __forceinline__ void abort_drain(volatile int* abort) {
+  if (*abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 50000ull) {
+    }
+  }
+}
+
 // mbar_wait for a barrier that another CTA of the cluster arrives on (what it did before is visible after).
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort,
                                                   int* status) {

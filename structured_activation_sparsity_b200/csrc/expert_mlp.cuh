@@ -301,6 +301,7 @@ __global__ void __launch_bounds__(kXThreads, 1)
     }
   }
   tc_fence_before();
+  abort_drain(abort);
   meet();   // (PAIR: nothing of the other CTA's is in use any more, either)
   if (warp == 1) {
     tc_fence_after();

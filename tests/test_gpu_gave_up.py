@@ -4,6 +4,7 @@ it ended, and the calls that follow, on the same shared memory, are right."""
 import pytest
 import torch
 
+import test_gpu_experts as G
 import test_gpu_norm as N
 from structured_activation_sparsity_b200 import _lib as L
 
@@ -46,4 +47,23 @@ def test_norms(hasty, rows, C, dtype, norms):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         for k in want[2]:
             assert want[2][k] is None or torch.equal(got[2][k], want[2][k]), k
+        assert L.sparsesam_device_status() == L.SS_OK
+
+
+@pytest.mark.parametrize("T,E,k,C,H", [(12, 4, 2, 64, 1024), (100, 4, 1, 256, 512), (900, 64, 2, 64, 1096),
+                                       (1100, 40, 2, 64, 2056), (1200, 4, 2, 256, 1024), (2000, 4, 2, 64, 4800)])
+def test_expert_mlp(hasty, T, E, k, C, H):
+    """Products by one CTA a tile (64 and 128 rows, with and without k-splits) and by pairs."""
+    v = G._mlp_inputs(T, E, k, C, H, 1)
+    ids = G._ids(T, E, k, 2)
+    cfg = L.make_expert_cfg(T, E, k, C=C, hidden=H)
+    want = G._mlp(cfg, v, ids)
+    assert L.sparsesam_device_status() == L.SS_OK
+    for _ in range(3):
+        hasty(1)
+        for _ in range(5):
+            G._mlp(cfg, v, ids)
+        assert L.sparsesam_device_status() in (L.SS_OK, L.SS_ETIMEOUT)
+        hasty(0)
+        assert torch.equal(G._mlp(cfg, v, ids), want)
         assert L.sparsesam_device_status() == L.SS_OK
