@@ -386,8 +386,8 @@ typedef struct {
  * is rounded once, n is the norm of x_out as stored (so it equals that of a separate call) and is
  * rounded once. stats (device) fp32 [rows, 4] or NULL: the post norm's mean and 1/sqrt, then the pre
  * norm's (0 for what is not there), which the backward reads. x_out may be x, and n may be y or x
- * (not x_out), with the same stride; nothing else may overlap. Errors: SS_EINVAL (a NULL, misaligned
- * or contradictory argument), SS_EUNSUPPORTED (C, rows). */
+ * (not x_out), with the same stride (else SS_EINVAL); nothing else may overlap. Errors: SS_EINVAL (a
+ * NULL, misaligned or contradictory argument), SS_EUNSUPPORTED (C, rows). */
 int sparsesam_norm_residual(const ss_norm_cfg* cfg, const void* y, const void* x, const void* gate,
                             const void* scale, const void* post_w, const void* post_b,
                             const void* pre_w, const void* pre_b, void* x_out, void* n,

@@ -107,6 +107,11 @@ int sparsesam_norm_residual(const ss_norm_cfg* cfg, const void* y, const void* x
     return SS_EINVAL;
   if (cfg->rows == 0) return SS_OK;
   if (!y || !x || !x_out || n == x_out) return SS_EINVAL;
+  // In place over y or x, n's rows have to be theirs: with another stride a row would be written over one
+  // that another block has yet to read.
+  const int64_t ld_n = or_C(cfg->ld_n, cfg->C);
+  if ((n == y && ld_n != or_C(cfg->ld_y, cfg->C)) || (n == x && ld_n != or_C(cfg->ld_x, cfg->C)))
+    return SS_EINVAL;
   const void* al[] = {y, x, gate, scale, post_w, post_b, pre_w, pre_b, x_out, n, stats};
   for (const void* a : al)
     if (!aligned(a, 16)) return SS_EINVAL;
