@@ -148,11 +148,11 @@ def _ptr(t) -> int | None:
 
 def _ptrs(*tensors):
     """_ptr of each (one pass: a call of a dozen pointers is on the path of small launches)."""
-    return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
+    return [t if t is None or isinstance(t, int) else t.data_ptr() for t in tensors]
 
 
 def _stream(stream) -> int | None:
-    if stream is None or stream.__class__ is int:
+    if stream is None or isinstance(stream, int):
         return stream
     return stream.cuda_stream  # torch.cuda.Stream
 
