@@ -1168,6 +1168,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
   }
   tc_fence_before();
+  abort_drain(abort);
   cta_sync_converged();
   if (warp == 1) {
     tc_fence_after();
