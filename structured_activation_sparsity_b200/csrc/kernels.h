@@ -214,11 +214,16 @@ struct NormParams {
   int C, center;                       // center: LayerNorm (else RMS norm)
   float eps;
 };
-// Up to this many warps of rows (one per 256 channels, rounded up to a power of two), the forward takes the
-// direct kernel. Measured on B200, direct / persistent: bf16 C 1280, 256 rows 4.5 / 5.7 us, 512 rows 8.0 / 5.7,
-// 1024 rows 14.6 / 5.7; C 64, 2048 rows 3.3 / 3.8, 4096 rows 5.0 / 4.0; C 4096, 148 rows 6.6 / 10.5, 256 rows
-// 12.0 / 10.6; fp32 C 1160, 256 rows 4.8 / 9.8, 512 rows 8.4 / 9.9.
-constexpr int kNormDirectWarps = 2560;
+// Up to this many warps of rows the forward takes the direct kernel; a row has `wide` warps (one per 256
+// channels, rounded up to a power of two). One wave of it (16 warps an SM), and two for fp32 rows of eight
+// warps, whose many-row kernel starts slowest. Measured on B200, direct / many-row, at 2048, 2560 and 4096 warps:
+// 16-bit C 64 3.3 / 3.7, 3.2 / 3.7, 4.8 / 3.7 us; C 1280 4.6 / 5.6, 7.4 / 5.6, 8.1 / 5.6; C 4096 6.6 / 10.6,
+// 12.2 / 10.6, 12.4 / 10.7; fp32 C 256 3.9 / 3.8, 3.9 / 5.5, 5.9 / 5.7; C 1160 4.9 / 9.7, 8.0 / 9.7, 8.8 / 9.7 (5120:
+// 11.9 / 9.7); C 4096 7.6 / 10.5, 14.0 / 10.5, 14.3 / 10.7.
+constexpr int kNormDirectWarps = 16 * kRowCtas;
+constexpr int norm_direct_warps(bool fp32, int wide) {
+  return fp32 && wide == 8 ? 2 * kNormDirectWarps : kNormDirectWarps;
+}
 cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cudaStream_t st);
 
 struct NormBwdParams {

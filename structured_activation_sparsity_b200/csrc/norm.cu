@@ -475,7 +475,7 @@ cudaError_t launch_norm_residual(const NormParams& p, int dtype, int* status, cu
     const int chunks = p.C / 8;
     int wide = 1;   // warps of a row at one chunk a lane
     while (wide * 32 < chunks) wide *= 2;
-    if (p.rows * wide <= kNormDirectWarps) {
+    if (p.rows * wide <= norm_direct_warps(T::kWords == 8, wide)) {
       const int wpr = wide;
       const int rpb = wpr < 4 ? 4 / wpr : 1;
       return launch_pdl(k_norm_residual_direct<T>, dim3((unsigned)((p.rows + rpb - 1) / rpb)),
