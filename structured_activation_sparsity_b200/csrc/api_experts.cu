@@ -60,7 +60,9 @@ int sort_launch(const int32_t* ids, int32_t* order, int32_t* slot, int32_t* offs
 }
 
 // sparsesam_expert_mlp's workspace: the sort's, the slots and offsets, the sorted rows, the hidden rows,
-// and fc2's rows (bf16, or fp32 partials when it is split along K).
+// and fc2's rows: bf16, or fp32 partials when it is split along K. (Whole rows in fp32 would take the result's
+// error from 0.00195 to 0.0018, of which the result's own rounding is 0.00165, and 16384 tokens of two experts
+// from 730 to 780 us: twice the bytes to write and to combine.)
 struct ExpertMlpLayout {
   ExpertGemmPlan fc1, fc2;
   size_t sort, slot, offsets, xs, h, y, total;
