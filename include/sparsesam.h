@@ -384,7 +384,8 @@ typedef struct {
  * [ceil(rows / rows_per_gate), C], scale, post_w, post_b, pre_w, pre_b (device) [C], the biases NULL for
  * zero; rows (device) as cfg says, all of cfg's dtype and 16-byte aligned. Norms and sums in fp32; x_out
  * is rounded once, n is the norm of x_out as stored (so it equals that of a separate call) and is
- * rounded once. stats (device) fp32 [rows, 4] or NULL: the post norm's mean and 1/sqrt, then the pre
+ * rounded once. A row's sums are added in an order that depends on C and on how many rows the call has:
+ * the same rows give the same bits in calls of the same shape. stats (device) fp32 [rows, 4] or NULL: the post norm's mean and 1/sqrt, then the pre
  * norm's (0 for what is not there), which the backward reads. x_out may be x, and n may be y or x
  * (not x_out), with the same stride (else SS_EINVAL); nothing else may overlap. Errors: SS_EINVAL (a
  * NULL, misaligned or contradictory argument), SS_EUNSUPPORTED (C, rows). */
