@@ -21,24 +21,23 @@ __device__ __forceinline__ float open_logit(float v) { return fmaxf(v, -INFINITY
 // 2^(p + q) = 2^p (1 + q ln 2), p the product of the rounded difference d and log2 e, q what p and d lost
 // (the difference's part by Knuth's exact sum: left out, it alone would cost |d| 2^-24). Past a distance
 // of 200, closed logits among them, it is 0. The pair's arithmetic is packed: on 39200 tokens of 64
-// experts the router and its gradient take 2.2 us more than with ex2 of the rounded product, and 3.2 with
+// experts the router and its gradient take 1.5 us more than with ex2 of the rounded product, and 3.2 with
 // expf and scalar sums.
 __device__ __forceinline__ void exp_below2(float v0, float v1, float top, float& e0, float& e1) {
   constexpr float kLog2e = 1.4426950408889634f, kLost = (float)(1.4426950408889634 - (double)kLog2e);
-  const bool far0 = v0 - top < -200.f, far1 = v1 - top < -200.f;
-  const uint64_t minus = f2_pack(-1.f, -1.f), t = f2_pack(top, top);
-  const uint64_t v = f2_pack(far0 ? top : v0, far1 ? top : v1);
+  const uint64_t minus = f2_pack(-1.f, -1.f), t = f2_pack(top, top), v = f2_pack(v0, v1);
   const uint64_t d = f2_fma(t, minus, v), b = f2_fma(v, minus, d);      // d = v - top, b = d - v
   const uint64_t r = f2_fma(f2_add(t, b), minus, f2_fma(f2_fma(b, minus, d), minus, v));
   const uint64_t l = f2_pack(kLog2e, kLog2e), p = f2_mul(d, l);
   uint64_t q = f2_fma(d, l, f2_mul(p, minus));
   q = f2_fma(d, f2_pack(kLost, kLost), f2_fma(r, l, q));
-  float p0, p1;
+  float p0, p1, d0, d1;
   f2_unpack(p, p0, p1);
+  f2_unpack(d, d0, d1);
   const uint64_t e = f2_pack(exp2f(p0), exp2f(p1));
   f2_unpack(f2_fma(e, f2_mul(q, f2_pack(0.69314718f, 0.69314718f)), e), e0, e1);
-  e0 = far0 ? 0.f : e0;
-  e1 = far1 ? 0.f : e1;
+  if (d0 < -200.f) e0 = 0.f;   // (q may be NaN there)
+  if (d1 < -200.f) e1 = 0.f;
 }
 __device__ __forceinline__ float exp_below(float v, float top) {
   float e, unused;
@@ -66,7 +65,7 @@ __device__ __forceinline__ float exps_below(float (&x)[V], float top, float (&e)
 // round of the top-k is a few compares and log2 L shuffles for several tokens at once, where a whole
 // warp a token spends two warp reductions on each. Each round takes the largest logit left and the lowest
 // expert that has it. Bound by instructions: 39200 tokens of 64 experts, four each, take about 7 us (10 MB read);
-// with their sort and the gradient 23.7 us.
+// with their sort and the gradient 25.8 us.
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
