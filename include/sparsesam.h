@@ -406,7 +406,8 @@ size_t sparsesam_norm_residual_backward_workspace(const ss_norm_cfg* cfg);
  * same inputs give the same bits); each may be NULL if it is not wanted, and is NULL where its
  * parameter is (dpost_b and dpre_b need post_w and pre_w only). They are written, not added to; with
  * no rows they are zero. dx may be dx_out, and dy may be y, else no output may overlap anything. ws
- * (device, 256-byte aligned) >= sparsesam_norm_residual_backward_workspace(cfg) bytes. */
+ * (device, 256-byte aligned) >= sparsesam_norm_residual_backward_workspace(cfg) bytes, its contents on
+ * entry do not matter; calls that may run at once need one each. */
 int sparsesam_norm_residual_backward(const ss_norm_cfg* cfg, const void* y, const void* x_out,
                                      const void* gate, const void* scale, const void* post_w,
                                      const void* post_b, const void* pre_w, const float* stats,
@@ -456,7 +457,8 @@ size_t sparsesam_expert_sort_workspace(const ss_expert_cfg* cfg);
  * order (device) int32 [n]: the assignment at each place, ascending within an expert; -1 at the places
  * past the last. slot (device) int32 [tokens, topk]: the inverse, each assignment's place or -1. Any of
  * the three outputs may be NULL (not all). ws (device, 256-byte aligned) >=
- * sparsesam_expert_sort_workspace(cfg) bytes. */
+ * sparsesam_expert_sort_workspace(cfg) bytes, its contents on entry do not matter; calls that may run at
+ * once need one each. */
 int sparsesam_expert_sort(const ss_expert_cfg* cfg, const int32_t* ids, int32_t* order,
                           int32_t* slot, int32_t* offsets, void* ws, size_t ws_bytes, void* stream);
 

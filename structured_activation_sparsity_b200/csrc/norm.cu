@@ -6,8 +6,8 @@
 //   n     = pre norm of x_out as stored         (what the next block reads)
 //
 // Every row is read and written once, all sums stay in fp32. Measured on B200 (HBM floor at the measured
-// copy rate in brackets): forward, 16384 rows of 1280 bf16 with everything on, 30.5 us (26.0); gradients,
-// 32768 rows of 1024 bf16, 80 us (62.4), 4039 rows of 1160 fp32, 34.7 us (17.4). What keeps them from the floor is
+// copy rate in brackets): forward, 16384 rows of 1280 bf16 with everything on, 30.8 us (26.0); gradients,
+// 32768 rows of 1024 bf16, 79 us (62.4), 4039 rows of 1160 fp32, 35 us (17.4). What keeps them from the floor is
 // the latency of the rows' sums and shared memory's bandwidth, not HBM.
 #include <type_traits>
 
